@@ -1,0 +1,429 @@
+"""Measured cases of the serving operators around the indexer: rotary positions, the E4M3
+quantisation of index queries and keys with its paged cache write, the read of a paged prefix,
+and latent attention in its absorbed (decode) and expanded (prefill) forms.
+
+`run` computes an operator in elementary torch operations, or, with `own` set, through the
+library's entry points. `exact` restates each definition in 64 bits, request by request.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+E4M3_MAX = 448.0
+TINY = torch.finfo(torch.float32).tiny
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+BLOCK = 64  # keys of a cache block, as the decode indexer takes them
+THETA = 10000.0
+LATENT, DV = 576, 512  # a cached latent row; its first 512 entries are the values
+NOPE, PE, VDIM = 128, 64, 128  # the expanded form's head
+
+
+# ------------------------------------------------------------------------------------- cases
+def listed():
+    return [
+        # the rotary part of 32 decode queries, 128 heads: a strided view of the absorbed queries
+        dict(name="rotary decode", op="rotary", T=32, H=128, d=64, rot=64, offset=0, row=576, interleaved=True,
+             factor=1.0, far=200000, dtype="bf16"),
+        # the index queries of a 16384-token prefill: first half of each 128-wide head is rotated
+        dict(name="rotary prefill", op="rotary", T=16384, H=64, d=128, rot=64, offset=0, row=128, interleaved=False,
+             factor=40.0, far=200000, dtype="bf16"),
+        # one decode step of 32 requests: 32 new index keys into the paged cache, rotated on the way
+        dict(name="index key write, decode", op="write", T=32, d=128, rot=64, offset=0, interleaved=False, blocks=4096,
+             skip=1, dtype="bf16"),
+        # the index queries of a 16384-token prefill, rotated and quantised per token over all heads
+        dict(name="index query quantise, prefill", op="quantise", T=16384, H=64, d=128, rot=64, offset=0,
+             interleaved=False, dtype="bf16"),
+        # the cached prefixes of 3 requests, codes and scales, as the next prefill chunk takes them
+        dict(name="index cache read, short", op="read", B=3, lo=100, hi=1500, lens_seed=3, values="none", d=128),
+        # 32 requests of 10000 to 200000 cached keys, read back as bf16 values
+        dict(name="index cache read, long", op="read", B=32, lo=10000, hi=200000, lens_seed=4, values="bf16", d=128),
+        # a small step: 4 short requests, 16 heads (a shard of 128)
+        dict(name="latent decode, short", op="decode", B=4, q_len=1, Hq=16, lo=60, hi=900, lens_seed=1, dtype="bf16"),
+        # two tokens a request (one drafted), 32 heads, ragged lengths
+        dict(name="latent decode, two tokens", op="decode", B=16, q_len=2, Hq=32, lo=1000, hi=12000, lens_seed=2,
+             dtype="f16"),
+        # 32 requests at 128 heads, long caches
+        dict(name="latent decode, long", op="decode", B=32, q_len=1, Hq=128, lo=10000, hi=40000, lens_seed=4,
+             dtype="bf16"),
+        # short prompts together, 16 heads
+        dict(name="latent prefill, ragged", op="prefill", B=5, H=16, lo=1, hi=400, past=0, lens_seed=5, dtype="bf16"),
+        # a 2048-token chunk behind 6144 earlier tokens, 16 heads
+        dict(name="latent prefill, chunk", op="prefill", B=1, H=16, lo=2048, hi=2048, past=6144, lens_seed=6,
+             dtype="f16"),
+        # a whole 8192-token prompt, 32 heads
+        dict(name="latent prefill, long", op="prefill", B=1, H=32, lo=8192, hi=8192, past=0, lens_seed=7,
+             dtype="bf16"),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["rotary", "write", "quantise", "read", "decode", "decode", "prefill", "prefill"])
+    half = rng.choice([True, False])
+    if op == "rotary":
+        d = rng.choice([64, 128, 192])
+        rot = rng.choice([32, 64])
+        return dict(op=op, T=_log_int(rng, 1, 16384), H=rng.choice([1, 8, 16, 64]), d=d, rot=rot,
+                    offset=rng.choice([0, d - rot]), row=d + rng.choice([0, 64]), interleaved=half,
+                    factor=rng.choice([1.0, 40.0]), far=rng.choice([4096, 200000]),
+                    dtype=rng.choice(["bf16", "f16", "f32"]))
+    if op == "write":
+        return dict(op=op, T=_log_int(rng, 1, 16384), d=128, rot=64, offset=rng.choice([0, 64]), interleaved=half,
+                    blocks=4096, skip=rng.randint(0, 3), dtype=rng.choice(["bf16", "f16", "f32"]))
+    if op == "quantise":
+        H, d = rng.choice([(64, 128), (8, 64)])
+        return dict(op=op, T=_log_int(rng, 1, 16384), H=H, d=d, rot=rng.choice([0, 32, 64]), offset=0, interleaved=half,
+                    dtype=rng.choice(["bf16", "f16", "f32"]))
+    if op == "read":
+        lo = _log_int(rng, 1, 10000)
+        return dict(op=op, B=rng.randint(1, 32), lo=lo, hi=min(200000, lo * rng.randint(1, 20)),
+                    lens_seed=rng.randint(0, 1 << 20), values=rng.choice(["none", "bf16", "f32"]), d=128)
+    if op == "decode":
+        lo = _log_int(rng, 1, 8000)
+        return dict(op=op, B=rng.randint(1, 32), q_len=rng.choice([1, 1, 1, 2, 4]), Hq=rng.choice([8, 16, 32, 64]),
+                    lo=lo, hi=min(16000, lo * rng.randint(1, 8)), lens_seed=rng.randint(0, 1 << 20),
+                    dtype=rng.choice(["bf16", "f16"]))
+    lo = _log_int(rng, 1, 2048)
+    return dict(op=op, B=rng.randint(1, 4), H=rng.choice([1, 4, 8, 16]), lo=lo, hi=min(2500, lo * rng.randint(1, 4)),
+                past=rng.choice([0, 0, rng.randint(1, 2000)]), lens_seed=rng.randint(0, 1 << 20),
+                dtype=rng.choice(["bf16", "f16"]))
+
+
+def _lens(case):
+    r = random.Random(case["lens_seed"])
+    return [r.randint(case["lo"], case["hi"]) for _ in range(case["B"])]
+
+
+def _pairs(case):
+    """Visible (query, key) pairs of a prefill case, all requests."""
+    return sum(n * case["past"] + n * (n + 1) // 2 for n in _lens(case))
+
+
+def work(case):
+    op, size = case["op"], {"bf16": 2, "f16": 2, "f32": 4, "none": 0}
+    if op == "rotary":
+        n = case["T"] * case["H"] * case["d"]
+        return {"bytes": 2 * n * size[case["dtype"]] + 4 * case["T"], "flops": 3 * case["T"] * case["H"] * case["rot"]}
+    if op in ("write", "quantise"):
+        n = case["T"] * case.get("H", 1) * case["d"]
+        return {"bytes": n * (size[case["dtype"]] + 1) + 8 * case["T"], "flops": 6 * n}
+    if op == "read":
+        n = sum(_lens(case))
+        return {"bytes": n * ((case["d"] + 4) * 2 if case["values"] == "none"
+                              else case["d"] * (1 + size[case["values"]]) + 4), "flops": n * case["d"]}
+    if op == "decode":
+        n, rows = sum(_lens(case)), case["B"] * case["q_len"] * case["Hq"]
+        return {"bytes": 2 * LATENT * n + 2 * (LATENT + DV) * rows + 4 * rows,
+                "flops": 2 * (LATENT + DV) * case["q_len"] * case["Hq"] * n}
+    nq = sum(_lens(case))
+    nk = nq + case["B"] * case["past"]
+    return {"bytes": 2 * (case["H"] * (nq * (NOPE + PE + VDIM) + nk * (NOPE + VDIM)) + nk * PE) + 4 * nq * case["H"],
+            "flops": 2 * (NOPE + PE + VDIM) * case["H"] * _pairs(case)}
+
+
+# ------------------------------------------------------------------------------------ inputs
+def _frequencies(rot, factor):
+    """Frequencies of a rotary part of `rot` dims; for factor > 1 the ones whose wavelength passes
+    the original 4096 tokens are divided by it, blended in between (YaRN's ramp, 32 to 1 turns)."""
+    half = rot // 2
+    f = [THETA ** (-i / half) for i in range(half)]
+    if factor == 1.0:
+        return f, 1.0
+    at = lambda turns: rot * math.log(4096 / (turns * 2 * math.pi)) / (2 * math.log(THETA))  # noqa: E731
+    low, high = max(math.floor(at(32.0)), 0), min(math.ceil(at(1.0)), rot - 1)
+    keep = [1.0 - min(1.0, max(0.0, (i - low) / max(high - low, 1e-3))) for i in range(half)]
+    return [x * k + x / factor * (1.0 - k) for x, k in zip(f, keep)], 0.1 * math.log(factor) + 1.0
+
+
+def _paged(lens, g, blocks_more=0):
+    """Block table and lengths of requests whose blocks are a random permutation of the cache's."""
+    nb = [(n + BLOCK - 1) // BLOCK for n in lens]
+    total = sum(nb) + blocks_more
+    perm = torch.randperm(total, generator=g, device="cuda").to(torch.int32)
+    table = torch.full((len(lens), max(max(nb), 1)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(nb):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table, torch.tensor(lens, dtype=torch.int32, device="cuda"), total
+
+
+def _activations(g, shape, dtype):
+    """Rows of N(0, 1) with a magnitude of their own a token."""
+    x = torch.randn(shape, generator=g, device="cuda")
+    size = torch.exp(0.5 * torch.randn((shape[0],) + (1,) * (len(shape) - 1), generator=g, device="cuda"))
+    return (x * size).to(DTYPES[dtype])
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    op, s = case["op"], dict(case=case)
+    if op in ("rotary", "write", "quantise"):
+        T, rot = case["T"], case["rot"]
+        if rot:
+            f, s["mscale"] = _frequencies(rot, case.get("factor", 1.0))
+            s["inv_freq"] = torch.tensor(f, dtype=torch.float64).to(torch.float32).cuda()
+            first = torch.randint(0, max(1, case.get("far", 200000) - T), (1,), generator=g, device="cuda")
+            s["positions"] = (first + torch.arange(T, device="cuda")).to(torch.int32)
+            if T <= 64:  # one token of each of T requests
+                s["positions"] = torch.randint(0, case.get("far", 200000), (T,), generator=g, device="cuda").to(torch.int32)
+    if op == "rotary":
+        s["x"] = _activations(g, (T, case["H"], case["row"]), case["dtype"])[..., case["row"] - case["d"]:]
+    elif op == "write":
+        s["x"] = _activations(g, (T, case["d"]), case["dtype"])
+        s["slots"] = torch.randperm(case["blocks"] * BLOCK, generator=g, device="cuda")[:T]
+        s["slots"][T - min(case["skip"], T - 1):] = -1  # padding at the batch's end
+        s["k_cache"] = torch.zeros(case["blocks"], BLOCK, case["d"], dtype=torch.uint8, device="cuda")
+        s["k_scale"] = torch.ones(case["blocks"], BLOCK, device="cuda")
+    elif op == "quantise":
+        s["x"] = _activations(g, (T, case["H"], case["d"]), case["dtype"])
+    elif op == "read":
+        lens = _lens(case)
+        s["table"], s["lens"], blocks = _paged(lens, g)
+        k = torch.randn(blocks, BLOCK, case["d"], generator=g, device="cuda") * 100.0
+        s["k_cache"] = k.clamp_(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn).view(torch.uint8)
+        s["k_scale"] = torch.rand(blocks, BLOCK, generator=g, device="cuda") * 0.01 + 0.001
+        s["cu"] = torch.tensor([0] + lens, dtype=torch.int64).cumsum(0).to(torch.int32).cuda()
+        s["total"] = sum(lens)
+    elif op == "decode":
+        s["table"], s["lens"], blocks = _paged(_lens(case), g)
+        s["q"] = torch.randn(case["B"], case["q_len"], case["Hq"], LATENT, generator=g, device="cuda").to(DTYPES[case["dtype"]])
+        s["latent"] = torch.randn(blocks * BLOCK, LATENT, generator=g, device="cuda", dtype=torch.float32).to(DTYPES[case["dtype"]])
+        s["scale"] = 2.0 / math.sqrt(LATENT)
+    else:
+        lens, H, dt = _lens(case), case["H"], DTYPES[case["dtype"]]
+        nq, nk = sum(lens), sum(lens) + case["past"] * len(lens)
+        s["q"] = torch.randn(nq, H, NOPE + PE, generator=g, device="cuda").to(dt)
+        kv = torch.randn(nk, H, NOPE + VDIM, generator=g, device="cuda").to(dt)  # the up-projection's output
+        s["k_nope"], s["v"] = kv[..., :NOPE], kv[..., NOPE:]
+        s["k_pe"] = torch.randn(nk, PE, generator=g, device="cuda").to(dt)
+        cu = torch.tensor([0] + lens).cumsum(0)
+        s["cu_q"] = cu.to(torch.int32).cuda()
+        s["cu_k"] = (cu + case["past"] * torch.arange(len(lens) + 1)).to(torch.int32).cuda()
+        s["max_q"] = max(lens)
+        s["max_k"] = max(lens) + case["past"]
+        s["scale"] = 2.0 / math.sqrt(NOPE + PE)
+    if own:
+        from sparse_attention_token_04_b200 import binding as B
+
+        nbytes = B.DSA_WS_HEADER_BYTES
+        if op == "decode":
+            nbytes = B.dsa_latent_attention_decode_workspace_bytes(case["B"], case["q_len"], case["Hq"])
+        s["ws"] = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    return s
+
+
+# --------------------------------------------------------------------------------- plain forms
+def _rotated(x, s, interleaved, offset, rot, mscale=1.0):
+    """x [T][H][d] rotated in fp32; the angles, up to 200000 radians, are formed in 64 bits."""
+    x = x.float()
+    ang = s["positions"].double()[:, None] * s["inv_freq"].double()[None, :]
+    cos, sin = (torch.cos(ang) * mscale).float()[:, None, :], (torch.sin(ang) * mscale).float()[:, None, :]
+    part = x[..., offset:offset + rot]
+    if interleaved:
+        a, b = part[..., 0::2], part[..., 1::2]
+        y = torch.stack((a * cos - b * sin, b * cos + a * sin), dim=-1).flatten(-2)
+    else:
+        a, b = part[..., :rot // 2], part[..., rot // 2:]
+        y = torch.cat((a * cos - b * sin, b * cos + a * sin), dim=-1)
+    return torch.cat((x[..., :offset], y, x[..., offset + rot:]), dim=-1)
+
+
+def _codes(x):
+    """x [T][n] -> E4M3 codes and the fp32 scale of each row: both quotients are fp32 numbers (the
+    first formed in 64 bits, where a division by a scalar is not turned into a multiplication)."""
+    top = x.abs().amax(dim=1)
+    scale = torch.where(top > 0, (top.double() / E4M3_MAX).float().clamp_min(TINY), torch.ones_like(top))
+    return (x / scale[:, None]).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn), scale
+
+
+def _plain(s):
+    c = s["case"]
+    op = c["op"]
+    if op == "rotary":
+        return _rotated(s["x"], s, c["interleaved"], c["offset"], c["rot"], s["mscale"]).to(s["x"].dtype)
+    if op == "write":
+        x = _rotated(s["x"][:, None], s, c["interleaved"], c["offset"], c["rot"])[:, 0]
+        codes, scale = _codes(x)
+        keep = s["slots"] >= 0
+        at = s["slots"][keep]
+        s["k_cache"].view(-1, c["d"])[at] = codes.view(torch.uint8)[keep]
+        s["k_scale"].view(-1)[at] = scale[keep]
+        return s["k_cache"].view(torch.float8_e4m3fn), s["k_scale"]
+    if op == "quantise":
+        x = _rotated(s["x"], s, c["interleaved"], c["offset"], c["rot"]) if c["rot"] else s["x"].float()
+        codes, scale = _codes(x.flatten(1))
+        return codes.view(x.shape), scale
+    if op == "read":
+        lens = s["lens"].long()
+        b = torch.repeat_interleave(torch.arange(c["B"], device="cuda"), lens, output_size=s["total"])
+        pos = torch.arange(s["total"], device="cuda") - s["cu"].long()[b]
+        row = s["table"][b, pos // BLOCK].long() * BLOCK + pos % BLOCK
+        codes, scale = s["k_cache"].view(-1, c["d"])[row], s["k_scale"].view(-1)[row]
+        if c["values"] == "none":
+            return codes.view(torch.float8_e4m3fn), scale
+        return (codes.view(torch.float8_e4m3fn).float() * scale[:, None]).to(DTYPES[c["values"]])
+    if op == "decode":
+        lens = s["lens"].long()
+        most = s["table"].shape[1] * BLOCK
+        pos = torch.arange(most, device="cuda")
+        row = (s["table"].clamp_min(0).long()[:, pos // BLOCK] * BLOCK + pos % BLOCK)
+        k = s["latent"][row].float()                                          # [B][most][576]
+        q = s["q"].float().flatten(1, 2)                                      # [B][q_len * Hq][576]
+        score = (q @ k.transpose(1, 2)) * s["scale"]
+        sees = lens[:, None] - c["q_len"] + 1 + torch.arange(c["q_len"], device="cuda")[None, :]
+        sees = sees.repeat_interleave(c["Hq"], dim=1)                         # keys a row sees
+        score = score.masked_fill(pos[None, None, :] >= sees[:, :, None], -math.inf)
+        top = score.amax(dim=2, keepdim=True).clamp_min(torch.finfo(torch.float32).min)
+        p = torch.exp(score - top)
+        total = p.sum(dim=2, keepdim=True)
+        o = torch.where(total > 0, (p @ k[..., :DV]) / total, torch.zeros_like(total))
+        lse = torch.where(total > 0, torch.log(total) + top, torch.full_like(total, -math.inf))
+        shape = (c["B"], c["q_len"], c["Hq"])
+        return o.view(shape + (DV,)).to(s["q"].dtype), lse.view(shape)
+    # prefill: requests padded to the longest
+    nq, nk = (s["cu_q"][1:] - s["cu_q"][:-1]).long(), (s["cu_k"][1:] - s["cu_k"][:-1]).long()
+    iq, ik = torch.arange(s["max_q"], device="cuda"), torch.arange(s["max_k"], device="cuda")
+    rq = (s["cu_q"][:-1].long()[:, None] + iq).clamp_max(s["q"].shape[0] - 1)
+    rk = (s["cu_k"][:-1].long()[:, None] + ik).clamp_max(s["k_pe"].shape[0] - 1)
+    q = s["q"][rq].float().transpose(1, 2)                                    # [B][H][max_q][192]
+    k = s["k_nope"][rk].float().transpose(1, 2)
+    pe = s["k_pe"][rk].float()[:, None]
+    score = (q[..., :NOPE] @ k.transpose(2, 3) + q[..., NOPE:] @ pe.transpose(2, 3)) * s["scale"]
+    hide = ik[None, None, :] > (iq[None, :] + (nk - nq)[:, None])[:, :, None]
+    score.masked_fill_((hide | (ik[None, None, :] >= nk[:, None, None]))[:, None], -math.inf)
+    top = score.amax(dim=3, keepdim=True)
+    p = torch.exp(score.sub_(top))
+    total = p.sum(dim=3, keepdim=True)
+    o = ((p @ s["v"][rk].float().transpose(1, 2)) / total).transpose(1, 2)    # [B][max_q][H][128]
+    lse = (torch.log(total) + top)[..., 0].transpose(1, 2)
+    real = iq[None, :] < nq[:, None]
+    return o[real].to(s["q"].dtype), lse[real]
+
+
+def _kernels(s):
+    from sparse_attention_token_04_b200 import binding as B
+
+    c = s["case"]
+    op = c["op"]
+    if op == "rotary":
+        return B.dsa_rotary(s["x"], s["positions"], s["inv_freq"], interleaved=c["interleaved"], rot_offset=c["offset"],
+                            mscale=s["mscale"])
+    turn = dict(positions=s["positions"], inv_freq=s["inv_freq"], interleaved=c["interleaved"],
+                rot_offset=c["offset"]) if c.get("rot") else {}
+    if op == "write":
+        B.dsa_index_cache_write(s["x"], s["slots"], s["k_cache"], s["k_scale"], workspace=s["ws"], **turn)
+        return s["k_cache"].view(torch.float8_e4m3fn), s["k_scale"]
+    if op == "quantise":
+        codes, scale = B.dsa_index_quantise(s["x"], workspace=s["ws"], **turn)
+        return codes.view(torch.float8_e4m3fn), scale
+    if op == "read":
+        if c["values"] == "none":
+            codes, scale, _ = B.dsa_index_cache_read(s["k_cache"], s["k_scale"], s["table"], s["cu"], s["total"],
+                                                     workspace=s["ws"])
+            return codes.view(torch.float8_e4m3fn), scale
+        return B.dsa_index_cache_read(s["k_cache"], s["k_scale"], s["table"], s["cu"], s["total"], want_codes=False,
+                                      values=DTYPES[c["values"]], workspace=s["ws"])[2]
+    if op == "decode":
+        return B.dsa_latent_attention_decode(s["q"], s["latent"], s["table"], s["lens"], s["scale"], block_size=BLOCK,
+                                             workspace=s["ws"])
+    return B.dsa_latent_attention_prefill(s["q"], s["k_nope"], s["k_pe"], s["v"], s["cu_q"], s["cu_k"], s["max_q"],
+                                          s["scale"], workspace=s["ws"])
+
+
+def run(state):
+    return _kernels(state) if own else _plain(state)
+
+
+# ------------------------------------------------------------------------- 64-bit definitions
+def _e4m3(y):
+    """The E4M3 value nearest to y (ties to even), |y| <= 448, from the format's step sizes."""
+    exponent = torch.floor(torch.log2(y.abs().clamp_min(2.0 ** -30))).clamp_min(-6.0)
+    step = torch.exp2(exponent - 3.0)
+    return torch.round(y / step) * step
+
+
+def _turn(x, c, s):
+    """Complex multiplication by exp(i pos f) of the pairs of x [T][H][d], in 64 bits."""
+    x = x.double().clone()
+    r = c["rot"]
+    lo = c["offset"]
+    if c["interleaved"]:
+        i0 = torch.arange(lo, lo + r, 2, device=x.device)
+        i1 = i0 + 1
+    else:
+        i0 = torch.arange(lo, lo + r // 2, device=x.device)
+        i1 = i0 + r // 2
+    w = torch.polar(torch.full((1, 1), float(s.get("mscale", 1.0)), dtype=torch.float64, device=x.device),
+                    s["positions"].double()[:, None] * s["inv_freq"].double()[None, :])[:, None, :]
+    z = torch.complex(x[..., i0], x[..., i1]) * w
+    x[..., i0], x[..., i1] = z.real, z.imag
+    return x
+
+
+def _attend(q, k, v, scale, sees):
+    """softmax(scale q k^T) v and its log-sum-exp for q [n][dk], k [m][dk], v [m][dv] in 64 bits;
+    query i sees the first sees[i] keys (a tensor)."""
+    score = scale * (q @ k.T)
+    score[torch.arange(k.shape[0], device=q.device)[None, :] >= sees[:, None]] = -math.inf
+    lse = torch.logsumexp(score, dim=1)
+    p = torch.exp(score - torch.where(torch.isinf(lse), torch.zeros_like(lse), lse)[:, None])
+    return p @ v, lse
+
+
+def exact(case, seed):
+    s, op = prepare(case, seed), case["op"]
+    if op == "rotary":
+        return _turn(s["x"], case, s)
+    if op in ("write", "quantise"):
+        x = s["x"][:, None] if op == "write" else s["x"]
+        x = _turn(x, case, s) if case["rot"] else x.double()
+        flat = x.reshape(x.shape[0], -1)
+        scale = flat.abs().max(dim=1).values / E4M3_MAX
+        scale = torch.where(scale > 0, scale, torch.ones_like(scale))
+        # codes stand for multiples of the scale that is stored, and the quotient is defined as an
+        # fp32 number: bf16 inputs meet exact ties between two codes often enough to tell
+        codes = _e4m3((flat / scale.float().double()[:, None]).float().double())
+        if op == "quantise":
+            return codes.view(x.shape), scale
+        cache = torch.zeros(case["blocks"] * BLOCK, case["d"], dtype=torch.float64, device="cuda")
+        scales = torch.ones(case["blocks"] * BLOCK, dtype=torch.float64, device="cuda")
+        n = int((s["slots"] >= 0).sum())  # the padding is at the end
+        cache[s["slots"][:n]], scales[s["slots"][:n]] = codes[:n], scale[:n]
+        return cache.view(case["blocks"], BLOCK, -1), scales.view(case["blocks"], BLOCK)
+    if op == "read":
+        codes, scales = [], []
+        for b, n in enumerate(_lens(case)):
+            blocks = s["table"][b, :(n + BLOCK - 1) // BLOCK].long()
+            codes.append(s["k_cache"][blocks].flatten(0, 1)[:n])
+            scales.append(s["k_scale"][blocks].flatten()[:n])
+        codes = torch.cat(codes).view(torch.float8_e4m3fn).double()
+        scales = torch.cat(scales).double()
+        return (codes, scales) if case["values"] == "none" else codes * scales[:, None]
+    out, lses = [], []
+    if op == "decode":
+        for b, n in enumerate(_lens(case)):
+            blocks = s["table"][b, :(n + BLOCK - 1) // BLOCK].long()
+            k = s["latent"].view(-1, BLOCK, LATENT)[blocks].flatten(0, 1)[:n].double()
+            sees = n - case["q_len"] + 1 + torch.arange(case["q_len"], device="cuda").repeat_interleave(case["Hq"])
+            o, lse = _attend(s["q"][b].flatten(0, 1).double(), k, k[:, :DV], s["scale"], sees)
+            out.append(o.view(case["q_len"], case["Hq"], DV))
+            lses.append(lse.view(case["q_len"], case["Hq"]))
+        return torch.stack(out), torch.stack(lses)
+    cq, ck = s["cu_q"].tolist(), s["cu_k"].tolist()
+    for b in range(case["B"]):
+        q, k = slice(cq[b], cq[b + 1]), slice(ck[b], ck[b + 1])
+        sees = (k.stop - k.start) - (q.stop - q.start) + 1 + torch.arange(q.stop - q.start, device="cuda")
+        heads = [_attend(s["q"][q, h].double(), torch.cat((s["k_nope"][k, h], s["k_pe"][k]), dim=1).double(),
+                         s["v"][k, h].double(), s["scale"], sees) for h in range(case["H"])]
+        out.append(torch.stack([o for o, _ in heads], dim=1))
+        lses.append(torch.stack([lse for _, lse in heads], dim=1))
+    return torch.cat(out), torch.cat(lses)
