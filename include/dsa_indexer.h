@@ -62,6 +62,9 @@ typedef enum dsa_status {
 
 enum { DSA_MODE_PREFILL = 0, DSA_MODE_DECODE = 1 };
 
+/* Element types of the entry points that take more than one. */
+enum { DSA_DTYPE_BF16 = 0, DSA_DTYPE_F16 = 1, DSA_DTYPE_F32 = 2 };
+
 /* Library ABI version (DSA_ABI_VERSION). */
 DSA_API int32_t dsa_abi_version(void);
 
@@ -283,6 +286,154 @@ DSA_API dsa_status dsa_sparse_attention_decode(const uint16_t* q, const uint16_t
                                                int32_t B, int32_t Hq, int32_t dqk, int32_t dv,
                                                int32_t topk, float scale, float* out,
                                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Rotary positions (the pages start from q and k that carry them and have no counterpart).
+ *
+ * Of every head of x [T][H][d], the `rot` dims from rot_offset on hold rot / 2 pairs (a, b); pair
+ * i of token t turns by the angle positions[t] * inv_freq[i]:
+ *     a' = mscale * (a cos - b sin),   b' = mscale * (b cos + a sin).
+ * interleaved = 0 pairs dim i with dim i + rot / 2, interleaved = 1 dims 2i and 2i + 1. inverse = 1
+ * turns by the negative angle: the gradient of the rotation, and its inverse for mscale = 1. The
+ * other dims are copied. Angles are formed in 64 bits, the products in fp32, and the result is
+ * rounded once to the element type.
+ *   x        [T][H][d] bf16, f16 or f32 (dtype), element strides x_stride_t, x_stride_h and 1
+ *   positions [T] i32, of either sign;  inv_freq [rot / 2] f32
+ *   out      [T][H][d] of x's type, strides out_stride_t, out_stride_h and 1. out may be x itself
+ *            (same pointer and strides); any other overlap of the two is not supported.
+ * T >= 0, H >= 1, 2 <= rot <= min(d, DSA_MAX_ROTARY), rot even, 0 <= rot_offset <= d - rot,
+ * H * d <= 2^20. Any alignment of the element type is taken; 16-byte aligned rows with rot and d
+ * multiples of 16 and rot_offset a multiple of 8 are the fast ones.
+ *
+ * dsa_rotary_frequencies (host): inv_freq[i] = theta^(-2i/rot), for factor > 1 scaled for contexts
+ * longer than original_len as the YaRN paper (Peng et al. 2023) does: frequencies that turn at most
+ * beta_slow times over original_len are divided by factor, those that turn at least beta_fast times
+ * are kept, with a linear ramp over the dims in between, and *mscale = 0.1 ln(factor) + 1 (else 1).
+ * inv_freq is a HOST array [rot / 2]; mscale may be NULL.
+ * -------------------------------------------------------------------------------------*/
+#define DSA_MAX_ROTARY 1024
+
+DSA_API dsa_status dsa_rotary(const void* x, int64_t x_stride_t, int64_t x_stride_h,
+                              const int32_t* positions, const float* inv_freq, int64_t T, int32_t H,
+                              int32_t d, int32_t rot, int32_t rot_offset, int32_t interleaved,
+                              int32_t inverse, float mscale, int32_t dtype, void* out,
+                              int64_t out_stride_t, int64_t out_stride_h, void* stream);
+
+DSA_API dsa_status dsa_rotary_frequencies(int32_t rot, double theta, double factor,
+                                          int32_t original_len, double beta_fast, double beta_slow,
+                                          float* inv_freq, float* mscale);
+
+/* ---------------------------------------------------------------------------------------
+ * The indexer's E4M3 inputs from real-valued queries and keys, and its paged key cache.
+ *
+ * A token's row of H * d values (d for a key) gets one scale, and its codes are
+ *     scale = max(absmax / 448, FLT_MIN), 1 for an all-zero row;   code = E4M3(value / scale),
+ * both quotients in fp32, the code rounded to nearest even. With positions given, the values are
+ * those of dsa_rotary, in fp32 and not rounded to x's type in between; positions = NULL quantises
+ * x as it is (inv_freq, rot, rot_offset, interleaved and mscale are then not read). A NaN counts as
+ * 0 and an infinity as the largest fp32 value; either is recorded as DSA_ERR_DEVICE.
+ *
+ * dsa_index_quantise writes the codes [T][H][d] and scale [T] that dsa_indexer_prefill (its q or,
+ * with H = 1, its k) and dsa_indexer_decode (q) take.
+ * dsa_index_cache_write writes key t at slots[t] of the paged cache that dsa_indexer_decode takes:
+ * slot block * block_size + offset, -1: the key is not written. A slot outside [-1, n_blocks *
+ * block_size) is recorded as DSA_ERR_DEVICE and not written. The slots of one call must be distinct
+ * (-1 aside): of two keys at the same slot, which one's codes and which one's scale remain is not
+ * defined. Nothing else of the cache is written.
+ *   x        [T][H][d] (dsa_index_quantise) or [T][d] bf16, f16 or f32 (dtype), element strides
+ *            x_stride_t, x_stride_h and 1; 16-byte aligned, strides multiples of 8 elements
+ *   slots    [T] i64
+ * T >= 0; d and rot multiples of 16, rot_offset a multiple of 8, H * d <= 16384 (else
+ * DSA_ERR_UNSUPPORTED).
+ *
+ * dsa_index_cache_read copies positions starts[b] .. starts[b] + n_b - 1 of every request b (n_b =
+ * cu_rows[b + 1] - cu_rows[b]; starts = NULL: from 0) from the paged cache to rows cu_rows[b] .. of
+ * the outputs: codes and scales as dsa_indexer_prefill takes its k, and / or their values code *
+ * scale. Each output may be NULL. Rows of [0, total) that belong to no request are left as they are,
+ * and none at total or behind it is written. A position whose table entry is missing or outside
+ * [0, n_blocks) is recorded as DSA_ERR_DEVICE and reads as zeros with scale 1.
+ *   cu_rows  [B + 1] i32, ascending;  starts [B] i32 or NULL
+ *   out_codes [total][d] u8, out_scale [total] f32, out_values [total][d] of values_dtype
+ *
+ * workspace of all three: >= DSA_WS_HEADER_BYTES bytes, 256-byte aligned (device-side status only).
+ * -------------------------------------------------------------------------------------*/
+DSA_API dsa_status dsa_index_quantise(const void* x, int64_t x_stride_t, int64_t x_stride_h, int64_t T,
+                                      int32_t H, int32_t d, int32_t dtype, const int32_t* positions,
+                                      const float* inv_freq, int32_t rot, int32_t rot_offset,
+                                      int32_t interleaved, float mscale, uint8_t* codes, float* scale,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+DSA_API dsa_status dsa_index_cache_write(const void* x, int64_t x_stride_t, int64_t T, int32_t d,
+                                         int32_t dtype, const int64_t* slots, const int32_t* positions,
+                                         const float* inv_freq, int32_t rot, int32_t rot_offset,
+                                         int32_t interleaved, float mscale, uint8_t* k_cache,
+                                         float* k_scale_cache, int32_t n_blocks, int32_t block_size,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_scale_cache,
+                                        int32_t n_blocks, int32_t block_size, int32_t d,
+                                        const int32_t* block_table, int32_t max_blocks,
+                                        const int32_t* starts, const int32_t* cu_rows, int32_t B,
+                                        int64_t total, uint8_t* out_codes, float* out_scale,
+                                        void* out_values, int32_t values_dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Latent attention over a whole context ("Index Share逻辑详解" §2 names the core MLA attention; a
+ * layer runs it dense where the context is not longer than top-k, and without an indexer always).
+ *
+ * Absorbed form, for 1 to 8 new tokens a request over the paged latent cache (the layout of
+ * dsa_sparse_attention_decode): for request b, new token i and head h, over the positions
+ * s < seq_lens[b] - q_len + 1 + i (the new tokens' latents are already cached, each sees itself),
+ *     out[b][i][h] = sum_s softmax_s(scale * q[b][i][h] . K[s]) K[s][0:512],
+ *     lse[b][i][h] = ln sum_s exp(scale * q[b][i][h] . K[s]).
+ * A token that sees nothing (seq_lens[b] <= q_len - 1 - i; 0 is a valid length) gets zeros and -inf.
+ *   q        [B][q_len][Hq][576], element strides q_stride_t (from one token to the next, request
+ *            after request), q_stride_h and 1, multiples of 8; 16-byte aligned
+ *   latent   [n_blocks * block_size][576], 16-byte aligned; rows at and behind a request's length
+ *            are not used, whatever they hold
+ *   block_table [B][max_blocks] i32 (entries past a request's last block are not read)
+ *   out      [B][q_len][Hq][512] of q's type;  lse [B][q_len][Hq] f32 or NULL
+ * dtype (of q, latent and out) is bf16 or f16. 1 <= q_len <= 8, 1 <= Hq <= 128, block_size a
+ * multiple of 8, dqk = 576 and dv = 512, else DSA_ERR_UNSUPPORTED. scale > 0. Products run on the
+ * tensor cores with fp32 accumulation; the softmax numerators are rounded to the element type before
+ * the value product, the sum and lse are taken over the unrounded ones. A length outside [0,
+ * max_blocks * block_size] is recorded as DSA_ERR_DEVICE and clamped, a block-table entry outside
+ * [0, n_blocks) is recorded and block 0 is read in its place.
+ * workspace: >= dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq) bytes, 256-byte aligned.
+ * -------------------------------------------------------------------------------------*/
+DSA_API size_t dsa_latent_attention_decode_workspace_bytes(int32_t B, int32_t q_len, int32_t Hq);
+
+DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                               const void* latent, int32_t n_blocks,
+                                               int32_t block_size, const int32_t* block_table,
+                                               int32_t max_blocks, const int32_t* seq_lens, int32_t B,
+                                               int32_t q_len, int32_t Hq, int32_t dqk, int32_t dv,
+                                               int32_t dtype, float scale, void* out, float* lse,
+                                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* Expanded form, for prefills: per-head keys (k_nope[h] | k_pe), k_pe shared by all heads, and
+ * per-head values, of requests laid end to end. Query i of request b (rows cu_q[b] .. cu_q[b+1]-1)
+ * sees keys cu_k[b] .. cu_k[b] + (n_k - n_q) + i with causal = 1 (the queries are the last n_q of the
+ * request's n_k tokens; n_k < n_q leaves the first ones nothing), and all n_k with causal = 0. lse
+ * joins the results of calls over disjoint parts of the keys. A query that sees nothing gets zeros
+ * and -inf; rows outside every request are left as they are.
+ *   q [Tq][H][192], k_nope [Tk][H][128], k_pe [Tk][64], v [Tk][H][128], bf16 or f16 (dtype), element
+ *   strides as named (token, head) and 1, multiples of 8; 16-byte aligned. k_nope and v may be
+ *   views of one [Tk][H][256] tensor.
+ *   cu_q, cu_k [B + 1] i32, ascending, within [0, Tq] and [0, Tk]; max_q >= every request's n_q
+ *   out [Tq][H][128] of q's type;  lse [Tq][H] f32 or NULL
+ * d_nope = 128, d_pe = 64 and dv = 128 (else DSA_ERR_UNSUPPORTED); scale > 0. Arithmetic as in the
+ * absorbed form. A request's values must be finite where any of its queries sees them. A request
+ * with bad offsets or more than max_q queries is recorded as DSA_ERR_DEVICE and left out.
+ * workspace: >= DSA_WS_HEADER_BYTES bytes, 256-byte aligned.
+ */
+DSA_API dsa_status dsa_latent_attention_prefill(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope, int64_t k_stride_t,
+    int64_t k_stride_h, const void* k_pe, int64_t pe_stride_t, const void* v, int64_t v_stride_t,
+    int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k, int32_t B, int32_t Tq, int32_t Tk,
+    int32_t max_q, int32_t H, int32_t d_nope, int32_t d_pe, int32_t dv, int32_t dtype, int32_t causal,
+    float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * Cross-layer top-k overlap ("IndexShare deep-dive report" §1.2: the overlap of layers i

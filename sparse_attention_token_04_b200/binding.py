@@ -27,8 +27,12 @@ DSA_ERR_DEVICE = 5
 DSA_MODE_PREFILL = 0
 DSA_MODE_DECODE = 1
 DSA_WS_HEADER_BYTES = 256
+DSA_DTYPE_BF16 = 0
+DSA_DTYPE_F16 = 1
+DSA_DTYPE_F32 = 2
 
 _i32, _u64, _sz, _vp = ctypes.c_int32, ctypes.c_uint64, ctypes.c_size_t, ctypes.c_void_p
+_i64, _f32, _f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
 
 
 class dsa_layer_inputs(ctypes.Structure):
@@ -74,6 +78,21 @@ _SIGNATURES = {
     "dsa_sparse_attention_workspace_bytes": (_sz, [_i32, _i32]),
     "dsa_sparse_attention_decode": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _i32, _i32,
                                            _i32, _i32, ctypes.c_float, _vp, _vp, _sz, _vp]),
+    "dsa_rotary": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32,
+                          _vp, _i64, _i64, _vp]),
+    "dsa_rotary_frequencies": (_i32, [_i32, _f64, _f64, _i32, _f64, _f64, _vp, _vp]),
+    "dsa_index_quantise": (_i32, [_vp, _i64, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _i32, _i32, _i32, _f32,
+                                  _vp, _vp, _vp, _sz, _vp]),
+    "dsa_index_cache_write": (_i32, [_vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _f32, _vp,
+                                     _vp, _i32, _i32, _vp, _sz, _vp]),
+    "dsa_index_cache_read": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp,
+                                    _vp, _i32, _vp, _sz, _vp]),
+    "dsa_latent_attention_decode_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "dsa_latent_attention_decode": (_i32, [_vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
+                                           _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
+    "dsa_latent_attention_prefill": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
+                                            _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                            _f32, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -485,3 +504,269 @@ def dsa_sparse_attention_decode(q, latent, block_table, seq_lens, idx, scale: fl
                                              _ptr(ws), ws.numel(), _stream(stream)),
            "dsa_sparse_attention_decode")
     return out
+
+
+_DTYPES = {torch.bfloat16: DSA_DTYPE_BF16, torch.float16: DSA_DTYPE_F16, torch.float32: DSA_DTYPE_F32}
+
+
+def _rows(t, name: str, dtypes, shape) -> None:
+    """A CUDA tensor of one of `dtypes` whose last dimension is contiguous (other strides are free)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+
+
+def _st(t, i: int) -> int:
+    """Stride of dimension i in elements; that of a dimension of one entry says nothing and is taken as 8."""
+    return t.stride(i) if t.shape[i] > 1 else 8
+
+
+class _On:
+    """Makes `device` (every tensor's) current and, where a stream other than the current one is
+    given, that stream too, so that what the call allocates belongs to the stream that uses it."""
+
+    def __init__(self, stream, first: torch.Tensor, *others):
+        for t in others:
+            if t is not None and t.device != first.device:
+                raise ValueError(f"tensors on {first.device} and {t.device}")
+        self.device, self.stream, self.held = first.device, stream, []
+
+    def __enter__(self):
+        if self.device.index != torch.cuda.current_device():
+            self._hold(torch.cuda.device(self.device))
+        now = torch.cuda.current_stream()
+        if self.stream is None:
+            return ctypes.c_void_p(now.cuda_stream)
+        raw = int(self.stream.cuda_stream if hasattr(self.stream, "cuda_stream") else self.stream)
+        if raw != now.cuda_stream:
+            other = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
+            self._hold(torch.cuda.stream(other))
+        return ctypes.c_void_p(raw)
+
+    def _hold(self, ctx):
+        ctx.__enter__()
+        self.held.append(ctx)
+
+    def __exit__(self, *exc):
+        while self.held:
+            self.held.pop().__exit__(*exc)
+        return False
+
+
+def _rotation(T: int, d: int, positions, inv_freq):
+    """rot dims of a call's rotation, 0 where no positions are given."""
+    if positions is None:
+        if inv_freq is not None:
+            raise ValueError("inv_freq without positions")
+        return 0
+    _need(positions, "positions", torch.int32, (T,))
+    _need(inv_freq, "inv_freq", torch.float32)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must have shape (rot // 2,)")
+    return 2 * int(inv_freq.shape[0])
+
+
+def dsa_rotary_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0, original_len: int = 4096,
+                           beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """Rotary frequencies (host): returns (inv_freq[rot // 2] f32 tensor on `device`, mscale), scaled
+    for contexts `factor` times as long as original_len where factor > 1."""
+    out = torch.empty(max(int(rot) // 2, 0), dtype=torch.float32)
+    m = ctypes.c_float(0.0)
+    _check(lib().dsa_rotary_frequencies(int(rot), float(theta), float(factor), int(original_len), float(beta_fast),
+                                        float(beta_slow), _ptr(out) if out.numel() else None, ctypes.byref(m)),
+           "dsa_rotary_frequencies")
+    return (out if device is None else out.to(device)), float(m.value)
+
+
+def dsa_rotary(x, positions, inv_freq, interleaved: bool = False, rot_offset: int = 0, mscale: float = 1.0,
+               inverse: bool = False, out=None, stream=None):
+    """Rotary positions: x[T][H][d] bf16 / f16 / f32 (last dimension contiguous), positions[T] i32,
+    inv_freq[rot // 2] f32 -> out like x, the dims [rot_offset, rot_offset + rot) of every head turned by
+    positions * inv_freq. out may be x; inverse turns back (the gradient of the rotation)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a tensor of shape (T, H, d)")
+    T, H, d = (int(n) for n in x.shape)
+    _rows(x, "x", _DTYPES, (T, H, d))
+    rot = _rotation(T, d, positions, inv_freq)
+    if rot == 0:
+        raise ValueError("positions and inv_freq are needed")
+    with _On(stream, x, positions, inv_freq, out) as s:
+        if out is None:
+            out = torch.empty(T, H, d, dtype=x.dtype, device=x.device)
+        _rows(out, "out", (x.dtype,), (T, H, d))
+        _check(lib().dsa_rotary(_ptr(x), _st(x, 0), _st(x, 1), _ptr(positions), _ptr(inv_freq), T, H, d, rot,
+                                int(rot_offset), int(interleaved), int(inverse), float(mscale), _DTYPES[x.dtype],
+                                _ptr(out), _st(out, 0), _st(out, 1), s), "dsa_rotary")
+    return out
+
+
+def dsa_index_quantise(x, positions=None, inv_freq=None, interleaved: bool = False, rot_offset: int = 0,
+                       mscale: float = 1.0, codes=None, scale=None, workspace=None, stream=None):
+    """E4M3 inputs of the indexer: x[T][H][d] (queries) or x[T][d] (keys) bf16 / f16 / f32, rotated where
+    positions are given -> (codes u8 of x's shape, scale[T] f32)."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
+        raise ValueError("x must be a tensor of shape (T, H, d) or (T, d)")
+    T, d = int(x.shape[0]), int(x.shape[-1])
+    H = int(x.shape[1]) if x.dim() == 3 else 1
+    _rows(x, "x", _DTYPES, x.shape)
+    rot = _rotation(T, d, positions, inv_freq)
+    with _On(stream, x, positions, inv_freq, codes, scale, workspace) as s:
+        if codes is None:
+            codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+        _need(codes, "codes", torch.uint8, x.shape)
+        if scale is None:
+            scale = torch.empty(T, dtype=torch.float32, device=x.device)
+        _need(scale, "scale", torch.float32, (T,))
+        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s.value or 0)
+        _check(lib().dsa_index_quantise(_ptr(x), _st(x, 0), _st(x, 1) if x.dim() == 3 else 8, T, H, d,
+                                        _DTYPES[x.dtype], _ptr(positions), _ptr(inv_freq), rot, int(rot_offset),
+                                        int(interleaved), float(mscale), _ptr(codes), _ptr(scale), _ptr(ws),
+                                        ws.numel(), s), "dsa_index_quantise")
+    return codes, scale
+
+
+def dsa_index_cache_write(x, slots, k_cache, k_scale_cache, positions=None, inv_freq=None, interleaved: bool = False,
+                          rot_offset: int = 0, mscale: float = 1.0, workspace=None, stream=None):
+    """Quantises keys x[T][d] bf16 / f16 / f32 (rotated where positions are given) into the paged cache
+    k_cache[n_blocks][block_size][d] u8, k_scale_cache[n_blocks][block_size] f32 at slots[T] i64 (-1: not
+    written)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a tensor of shape (T, d)")
+    T, d = (int(n) for n in x.shape)
+    _rows(x, "x", _DTYPES, (T, d))
+    n_blocks, block_size = int(k_cache.shape[0]), int(k_cache.shape[1])
+    _need(slots, "slots", torch.int64, (T,))
+    _need(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
+    _need(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
+    rot = _rotation(T, d, positions, inv_freq)
+    with _On(stream, x, slots, k_cache, k_scale_cache, positions, inv_freq, workspace) as s:
+        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s.value or 0)
+        _check(lib().dsa_index_cache_write(_ptr(x), _st(x, 0), T, d, _DTYPES[x.dtype], _ptr(slots), _ptr(positions),
+                                           _ptr(inv_freq), rot, int(rot_offset), int(interleaved), float(mscale),
+                                           _ptr(k_cache), _ptr(k_scale_cache), n_blocks, block_size, _ptr(ws),
+                                           ws.numel(), s), "dsa_index_cache_write")
+
+
+def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: int, starts=None,
+                         want_codes: bool = True, values=None, out_codes=None, out_scale=None, out_values=None,
+                         workspace=None, stream=None):
+    """Reads request ranges of the paged key cache: rows cu_rows[b] .. cu_rows[b + 1] of the outputs are
+    positions starts[b] .. (0 .. without starts) of request b -> (codes[total][d] u8, scale[total] f32,
+    values[total][d] of the type `values`), the first two None without want_codes, the last without values."""
+    n_blocks, block_size, d = (int(n) for n in k_cache.shape)
+    B = int(block_table.shape[0])
+    total = int(total)
+    _need(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
+    _need(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
+    _need(block_table, "block_table", torch.int32, (B, int(block_table.shape[1])))
+    _need(cu_rows, "cu_rows", torch.int32, (B + 1,))
+    if starts is not None:
+        _need(starts, "starts", torch.int32, (B,))
+    if out_values is not None and values is None:
+        values = out_values.dtype
+    if values is not None and values not in _DTYPES:
+        raise ValueError(f"values must be one of {[str(t) for t in _DTYPES]}, got {values}")
+    dev = k_cache.device
+    with _On(stream, k_cache, k_scale_cache, block_table, cu_rows, starts, out_codes, out_scale, out_values,
+             workspace) as s:
+        if want_codes and out_codes is None:
+            out_codes = torch.empty(total, d, dtype=torch.uint8, device=dev)
+        if want_codes and out_scale is None:
+            out_scale = torch.empty(total, dtype=torch.float32, device=dev)
+        if values is not None and out_values is None:
+            out_values = torch.empty(total, d, dtype=values, device=dev)
+        if out_codes is not None:
+            _need(out_codes, "out_codes", torch.uint8, (total, d))
+        if out_scale is not None:
+            _need(out_scale, "out_scale", torch.float32, (total,))
+        if out_values is not None:
+            _need(out_values, "out_values", values, (total, d))
+        ws = _workspace(DSA_WS_HEADER_BYTES, dev, workspace, s.value or 0)
+        _check(lib().dsa_index_cache_read(_ptr(k_cache), _ptr(k_scale_cache), n_blocks, block_size, d,
+                                          _ptr(block_table), int(block_table.shape[1]), _ptr(starts), _ptr(cu_rows),
+                                          B, total, _ptr(out_codes), _ptr(out_scale), _ptr(out_values),
+                                          _DTYPES.get(values, DSA_DTYPE_F32), _ptr(ws), ws.numel(), s),
+               "dsa_index_cache_read")
+    return out_codes, out_scale, out_values
+
+
+def dsa_latent_attention_decode_workspace_bytes(B: int, q_len: int, Hq: int) -> int:
+    return int(lib().dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq))
+
+
+def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, block_size: int = 64, out=None,
+                                lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Dense latent attention of 1 to 8 new tokens a request over the paged latents (absorbed form):
+    q[B][q_len][Hq][576] or q[B][Hq][576] bf16 / f16, latent[n_blocks * block_size][576],
+    block_table[B][max_blocks] i32, seq_lens[B] i32 -> (out like q with 512 dims, lse[B][q_len][Hq] or
+    [B][Hq] f32)."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a tensor of shape (B, q_len, Hq, 576) or (B, Hq, 576)")
+    q4 = q if q.dim() == 4 else q[:, None]
+    B, q_len, Hq, dqk = (int(n) for n in q4.shape)
+    half = (torch.bfloat16, torch.float16)
+    _rows(q, "q", half, q.shape)
+    if B > 1 and q_len > 1 and q4.stride(0) != q_len * q4.stride(1):
+        raise ValueError("q's tokens must be evenly spaced over its requests")
+    q_stride_t = _st(q4, 1) if q_len > 1 else _st(q4, 0)
+    n_rows, dv = int(latent.shape[0]), 512
+    _need(latent, "latent", q.dtype, (n_rows, dqk))
+    _need(block_table, "block_table", torch.int32, (B, int(block_table.shape[1])))
+    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    if block_size < 1 or n_rows % block_size:
+        raise ValueError("latent rows must be whole blocks")
+    with _On(stream, q, latent, block_table, seq_lens, out, lse, workspace) as s:
+        if out is None:
+            out = torch.empty(q.shape[:-1] + (dv,), dtype=q.dtype, device=q.device)
+        _need(out, "out", q.dtype, q.shape[:-1] + (dv,))
+        if lse is None and want_lse:
+            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _need(lse, "lse", torch.float32, q.shape[:-1])
+        ws = _workspace(dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq), q.device, workspace, s.value or 0)
+        _check(lib().dsa_latent_attention_decode(_ptr(q), q_stride_t, _st(q4, 2), _ptr(latent), n_rows // block_size,
+                                                 block_size, _ptr(block_table), int(block_table.shape[1]),
+                                                 _ptr(seq_lens), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], float(scale),
+                                                 _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s),
+               "dsa_latent_attention_decode")
+    return out, lse
+
+
+def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, causal: bool = True,
+                                 out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Latent attention of ragged prefills (expanded form): q[Tq][H][192], k_nope[Tk][H][128], k_pe[Tk][64],
+    v[Tk][H][128] bf16 / f16 (last dimensions contiguous), request offsets cu_q, cu_k [B + 1] i32, at most
+    max_q queries a request -> (out[Tq][H][128], lse[Tq][H] f32)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor of shape (Tq, H, 192)")
+    Tq, H, dqk = (int(n) for n in q.shape)
+    half = (torch.bfloat16, torch.float16)
+    _rows(q, "q", half, (Tq, H, dqk))
+    Tk, d_nope, d_pe, dv = int(k_pe.shape[0]), int(k_nope.shape[-1]), int(k_pe.shape[-1]), int(v.shape[-1])
+    _rows(k_nope, "k_nope", (q.dtype,), (Tk, H, d_nope))
+    _rows(k_pe, "k_pe", (q.dtype,), (Tk, d_pe))
+    _rows(v, "v", (q.dtype,), (Tk, H, dv))
+    if d_nope + d_pe != dqk:
+        raise ValueError("q's heads must be as wide as k_nope's and k_pe together")
+    _need(cu_q, "cu_q", torch.int32)
+    _need(cu_k, "cu_k", torch.int32, cu_q.shape)
+    with _On(stream, q, k_nope, k_pe, v, cu_q, cu_k, out, lse, workspace) as s:
+        if out is None:
+            out = torch.empty(Tq, H, dv, dtype=q.dtype, device=q.device)
+        _need(out, "out", q.dtype, (Tq, H, dv))
+        if lse is None and want_lse:
+            lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
+        if lse is not None:
+            _need(lse, "lse", torch.float32, (Tq, H))
+        ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s.value or 0)
+        _check(lib().dsa_latent_attention_prefill(
+            _ptr(q), _st(q, 0), _st(q, 1), _ptr(k_nope), _st(k_nope, 0), _st(k_nope, 1), _ptr(k_pe),
+            _st(k_pe, 0), _ptr(v), _st(v, 0), _st(v, 1), _ptr(cu_q), _ptr(cu_k), int(cu_q.numel()) - 1, Tq, Tk,
+            int(max_q), H, d_nope, d_pe, dv, _DTYPES[q.dtype], int(causal), float(scale), _ptr(out), _ptr(lse),
+            _ptr(ws), ws.numel(), s), "dsa_latent_attention_prefill")
+    return out, lse

@@ -59,6 +59,34 @@ dsa_status check_decode(const uint8_t* q, const float* q_scale, const float* w,
   return DSA_OK;
 }
 
+bool good_scale(float scale) { return scale > 0.0f && scale < 1e30f; }
+
+// Strides (elements) that keep 16-byte rows 16-byte aligned.
+bool wide_strides(int64_t a, int64_t b) { return a > 0 && b > 0 && a % 8 == 0 && b % 8 == 0; }
+
+// The rotation of a quantising call; positions = NULL means none.
+dsa_status check_quantise(const void* x, int64_t xs_t, int64_t xs_h, int64_t T, int32_t H, int32_t d,
+                          int32_t dtype, const int32_t* positions, const float* inv_freq, int32_t rot,
+                          int32_t rot_offset, int32_t interleaved, float mscale, const uint8_t* codes,
+                          const float* scale, const void* workspace, size_t workspace_bytes,
+                          RotaryArgs* r) {
+  if (T < 0 || T > INT32_MAX || H < 1 || d < 1) return DSA_ERR_INVALID;
+  if (dtype < DSA_DTYPE_BF16 || dtype > DSA_DTYPE_F32) return DSA_ERR_INVALID;
+  if (T > 0 && (!x || !codes || !scale)) return DSA_ERR_INVALID;
+  if (!aligned(x, 16) || !aligned(codes, 8) || !wide_strides(xs_t, xs_h)) return DSA_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < DSA_WS_HEADER_BYTES) return DSA_ERR_INVALID;
+  *r = RotaryArgs{};
+  if (positions) {
+    if (!inv_freq || rot < 2 || rot % 2 || rot > d || rot_offset < 0 || rot_offset > d - rot ||
+        !(mscale > -1e30f && mscale < 1e30f))
+      return DSA_ERR_INVALID;
+    if (rot % 16 || rot_offset % 8 || rot > DSA_MAX_ROTARY) return DSA_ERR_UNSUPPORTED;
+    *r = RotaryArgs{positions, inv_freq, rot, rot_offset, interleaved != 0, 0, mscale};
+  }
+  if (d % 16 || static_cast<int64_t>(H) * d > kQuantMaxRow) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
 }  // namespace
 
 bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
@@ -200,6 +228,155 @@ DSA_API dsa_status dsa_sparse_attention_decode(const uint16_t* q, const uint16_t
   AttentionLaunch a{q, latent, n_blocks, block_size, block_table, max_blocks, seq_lens, idx, B, topk,
                     scale, out, workspace, static_cast<cudaStream_t>(stream), wait_budget_ns()};
   return launch_attention(a);
+}
+
+DSA_API dsa_status dsa_rotary(const void* x, int64_t x_stride_t, int64_t x_stride_h,
+                              const int32_t* positions, const float* inv_freq, int64_t T, int32_t H,
+                              int32_t d, int32_t rot, int32_t rot_offset, int32_t interleaved,
+                              int32_t inverse, float mscale, int32_t dtype, void* out,
+                              int64_t out_stride_t, int64_t out_stride_h, void* stream) {
+  if (T < 0 || T > INT32_MAX || H < 1 || d < 2 || rot < 2 || rot % 2 || rot > d || rot_offset < 0 ||
+      rot_offset > d - rot)
+    return DSA_ERR_INVALID;
+  if (dtype < DSA_DTYPE_BF16 || dtype > DSA_DTYPE_F32 || !(mscale > -1e30f && mscale < 1e30f))
+    return DSA_ERR_INVALID;
+  if (x_stride_t < 0 || x_stride_h < 0 || out_stride_t < 1 || out_stride_h < 1) return DSA_ERR_INVALID;
+  if (rot > DSA_MAX_ROTARY || static_cast<int64_t>(H) * d > (1 << 20)) return DSA_ERR_UNSUPPORTED;
+  if (T == 0) return DSA_OK;
+  const uintptr_t size = dtype == DSA_DTYPE_F32 ? 4 : 2;
+  if (!x || !positions || !inv_freq || !out || !aligned(x, size) || !aligned(out, size)) return DSA_ERR_INVALID;
+  const int sms = current_num_sms();
+  if (sms < 1) return DSA_ERR_CUDA;
+  RotaryLaunch a{{positions, inv_freq, rot, rot_offset, interleaved != 0, inverse != 0, mscale},
+                 x, x_stride_t, x_stride_h, out, out_stride_t, out_stride_h, T, H, d, dtype,
+                 static_cast<cudaStream_t>(stream), sms};
+  return launch_rotary(a);
+}
+
+DSA_API dsa_status dsa_rotary_frequencies(int32_t rot, double theta, double factor,
+                                          int32_t original_len, double beta_fast, double beta_slow,
+                                          float* inv_freq, float* mscale) {
+  if (!inv_freq || rot < 2 || rot % 2 || !(theta > 1.0 && theta < 1e30) || !(factor >= 1.0 && factor < 1e30) ||
+      original_len < 1 || !(beta_slow > 0.0 && beta_fast >= beta_slow && beta_fast < 1e30))
+    return DSA_ERR_INVALID;
+  rotary_frequencies(rot, theta, factor, original_len, beta_fast, beta_slow, inv_freq, mscale);
+  return DSA_OK;
+}
+
+DSA_API dsa_status dsa_index_quantise(const void* x, int64_t x_stride_t, int64_t x_stride_h, int64_t T,
+                                      int32_t H, int32_t d, int32_t dtype, const int32_t* positions,
+                                      const float* inv_freq, int32_t rot, int32_t rot_offset,
+                                      int32_t interleaved, float mscale, uint8_t* codes, float* scale,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  RotaryArgs r;
+  dsa_status st = check_quantise(x, x_stride_t, x_stride_h, T, H, d, dtype, positions, inv_freq, rot,
+                                 rot_offset, interleaved, mscale, codes, scale, workspace,
+                                 workspace_bytes, &r);
+  if (st != DSA_OK || T == 0) return st;
+  const QuantParams p{r, x, x_stride_t, x_stride_h, T, H, d, nullptr, 0, codes, scale,
+                      static_cast<WsHeader*>(workspace)};
+  return launch_quantise(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+DSA_API dsa_status dsa_index_cache_write(const void* x, int64_t x_stride_t, int64_t T, int32_t d,
+                                         int32_t dtype, const int64_t* slots, const int32_t* positions,
+                                         const float* inv_freq, int32_t rot, int32_t rot_offset,
+                                         int32_t interleaved, float mscale, uint8_t* k_cache,
+                                         float* k_scale_cache, int32_t n_blocks, int32_t block_size,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  if (n_blocks < 1 || block_size < 1 || static_cast<int64_t>(n_blocks) * block_size > INT32_MAX)
+    return DSA_ERR_INVALID;
+  if (T > 0 && !slots) return DSA_ERR_INVALID;
+  RotaryArgs r;
+  dsa_status st = check_quantise(x, x_stride_t, 8, T, 1, d, dtype, positions, inv_freq, rot, rot_offset,
+                                 interleaved, mscale, k_cache, k_scale_cache, workspace,
+                                 workspace_bytes, &r);
+  if (st != DSA_OK || T == 0) return st;
+  const QuantParams p{r, x, x_stride_t, 0, T, 1, d, slots, static_cast<int64_t>(n_blocks) * block_size,
+                      k_cache, k_scale_cache, static_cast<WsHeader*>(workspace)};
+  return launch_quantise(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_scale_cache,
+                                        int32_t n_blocks, int32_t block_size, int32_t d,
+                                        const int32_t* block_table, int32_t max_blocks,
+                                        const int32_t* starts, const int32_t* cu_rows, int32_t B,
+                                        int64_t total, uint8_t* out_codes, float* out_scale,
+                                        void* out_values, int32_t values_dtype, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  if (!k_cache || !k_scale_cache || !block_table || !cu_rows) return DSA_ERR_INVALID;
+  if (n_blocks < 1 || block_size < 1 || d < 1 || max_blocks < 1 || B < 1 || total < 0 || total > INT32_MAX)
+    return DSA_ERR_INVALID;
+  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX ||
+      static_cast<int64_t>(n_blocks) * block_size > INT32_MAX)
+    return DSA_ERR_INVALID;
+  if (values_dtype < DSA_DTYPE_BF16 || values_dtype > DSA_DTYPE_F32) return DSA_ERR_INVALID;
+  if (!aligned(k_cache, 16) || !aligned(out_codes, 16) || !aligned(out_values, 16)) return DSA_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < DSA_WS_HEADER_BYTES) return DSA_ERR_INVALID;
+  if (d % 16 || d > kQuantMaxRow) return DSA_ERR_UNSUPPORTED;
+  if (total == 0 || (!out_codes && !out_scale && !out_values)) return DSA_OK;
+  const ReadParams p{k_cache, k_scale_cache, n_blocks, block_size, d, block_table, max_blocks, starts,
+                     cu_rows, B, total, out_codes, out_scale, out_values, static_cast<WsHeader*>(workspace)};
+  return launch_cache_read(p, values_dtype, static_cast<cudaStream_t>(stream));
+}
+
+DSA_API size_t dsa_latent_attention_decode_workspace_bytes(int32_t B, int32_t q_len, int32_t Hq) {
+  if (B < 1 || B > DSA_DECODE_MAX_REQUESTS || q_len < 1 || q_len > 8 || Hq < 1 || Hq > 128) return 0;
+  return latent_decode_workspace_bytes(B, q_len, Hq);
+}
+
+DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                               const void* latent, int32_t n_blocks,
+                                               int32_t block_size, const int32_t* block_table,
+                                               int32_t max_blocks, const int32_t* seq_lens, int32_t B,
+                                               int32_t q_len, int32_t Hq, int32_t dqk, int32_t dv,
+                                               int32_t dtype, float scale, void* out, float* lse,
+                                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !latent || !block_table || !seq_lens || !out) return DSA_ERR_INVALID;
+  if (B < 1 || q_len < 1 || Hq < 1 || n_blocks < 1 || block_size < 1 || max_blocks < 1) return DSA_ERR_INVALID;
+  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX ||
+      static_cast<int64_t>(n_blocks) * block_size > INT32_MAX)
+    return DSA_ERR_INVALID;
+  if (!good_scale(scale) || !wide_strides(q_stride_t, q_stride_h)) return DSA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(latent, 16) || !aligned(out, 16)) return DSA_ERR_INVALID;
+  if (dqk != 576 || dv != 512 || (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F16) || q_len > 8 ||
+      Hq > 128 || block_size % 8 || B > DSA_DECODE_MAX_REQUESTS)
+    return DSA_ERR_UNSUPPORTED;
+  if (!workspace || !aligned(workspace, 256)) return DSA_ERR_INVALID;
+  if (workspace_bytes < latent_decode_workspace_bytes(B, q_len, Hq)) return DSA_ERR_INVALID;
+  const int sms = current_num_sms();
+  if (sms < 1) return DSA_ERR_CUDA;
+  const LatentDecodeParams p{q, q_stride_t, q_stride_h, latent, n_blocks, block_size, block_table,
+                             max_blocks, seq_lens, B, q_len, Hq, scale, out, lse,
+                             static_cast<WsHeader*>(workspace), wait_budget_ns(), sms};
+  return launch_latent_decode(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+DSA_API dsa_status dsa_latent_attention_prefill(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope, int64_t k_stride_t,
+    int64_t k_stride_h, const void* k_pe, int64_t pe_stride_t, const void* v, int64_t v_stride_t,
+    int64_t v_stride_h, const int32_t* cu_q, const int32_t* cu_k, int32_t B, int32_t Tq, int32_t Tk,
+    int32_t max_q, int32_t H, int32_t d_nope, int32_t d_pe, int32_t dv, int32_t dtype, int32_t causal,
+    float scale, void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cu_q || !cu_k || B < 1 || Tq < 0 || Tk < 0 || max_q < 0 || H < 1) return DSA_ERR_INVALID;
+  if (!good_scale(scale) || !wide_strides(q_stride_t, q_stride_h) || !wide_strides(k_stride_t, k_stride_h) ||
+      !wide_strides(v_stride_t, v_stride_h) || !wide_strides(pe_stride_t, 8))
+    return DSA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(k_nope, 16) || !aligned(k_pe, 16) || !aligned(v, 16) || !aligned(out, 16))
+    return DSA_ERR_INVALID;
+  if (Tq > 0 && (!q || !out)) return DSA_ERR_INVALID;
+  if (Tk > 0 && (!k_nope || !k_pe || !v)) return DSA_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < DSA_WS_HEADER_BYTES) return DSA_ERR_INVALID;
+  if (d_nope != 128 || d_pe != 64 || dv != 128 || (dtype != DSA_DTYPE_BF16 && dtype != DSA_DTYPE_F16) ||
+      H > 65535 || B > 65535)
+    return DSA_ERR_UNSUPPORTED;
+  if (Tq == 0 || max_q == 0) return DSA_OK;
+  const int sms = current_num_sms();
+  if (sms < 1) return DSA_ERR_CUDA;
+  const LatentPrefillParams p{q, q_stride_t, q_stride_h, k_nope, k_stride_t, k_stride_h, k_pe, pe_stride_t,
+                              v, v_stride_t, v_stride_h, cu_q, cu_k, B, Tq, Tk, max_q, H, causal != 0, scale,
+                              out, lse, static_cast<WsHeader*>(workspace), wait_budget_ns(), sms};
+  return launch_latent_prefill(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API size_t dsa_indexcache_workspace_bytes(const dsa_indexer_shape* shape) {

@@ -42,6 +42,8 @@ enum : uint32_t {
   DETAIL_BAD_SEQ_LEN = 17,
   DETAIL_BAD_INDEX = 18,
   DETAIL_HIST_MISMATCH = 19,
+  DETAIL_BAD_SLOT = 20,
+  DETAIL_NOT_FINITE = 21,
 };
 
 __device__ __forceinline__ void record_error(WsHeader* hdr, uint32_t status, uint32_t detail) {

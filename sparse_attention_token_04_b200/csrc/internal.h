@@ -10,6 +10,8 @@
 
 namespace dsa {
 
+struct WsHeader;
+
 struct PrefillLaunch {
   const uint8_t* q;
   const float* q_scale;
@@ -148,6 +150,101 @@ dsa_status launch_decode_topk(void* ws, const DecodeLayout& lay, int max_len,
 // Sparse attention of decode queries over their selected latents (attention.cu).
 size_t attention_workspace_bytes(int B, int topk);
 dsa_status launch_attention(const AttentionLaunch& a);
+
+// Rotary positions (rotary.cu): pair i of a token at position p turns by p * inv_freq[i].
+struct RotaryArgs {
+  const int32_t* positions;
+  const float* inv_freq;
+  int32_t rot, offset;          // dims of the rotary part and where it starts in a head
+  int32_t interleaved, inverse;
+  float mscale;
+};
+struct RotaryLaunch {
+  RotaryArgs r;
+  const void* x;
+  int64_t xs_t, xs_h;           // strides in elements: token, head
+  void* out;
+  int64_t os_t, os_h;
+  int64_t T;
+  int32_t H, d, dtype;
+  cudaStream_t stream;
+  int num_sms;
+};
+dsa_status launch_rotary(const RotaryLaunch& a);
+void rotary_frequencies(int rot, double theta, double factor, int original_len, double beta_fast,
+                        double beta_slow, float* inv_freq, float* mscale);
+
+// Quantisation of index queries and keys and the paged key cache (index_cache.cu). A row is a
+// token's H x d values; r.rot = 0 quantises without a rotation.
+constexpr int kQuantMaxRow = 16384;
+struct QuantParams {
+  RotaryArgs r;
+  const void* x;
+  int64_t xs_t, xs_h;
+  int64_t T;
+  int32_t H, d;
+  const int64_t* slots;         // row t goes to slots[t] (-1: nowhere), or to t if NULL
+  int64_t n_slots;
+  uint8_t* codes;
+  float* scale;
+  WsHeader* hdr;
+};
+dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream);
+struct ReadParams {
+  const uint8_t* k_cache;
+  const float* k_scale_cache;
+  int32_t n_blocks, block_size, d;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  const int32_t* starts;        // first position of each request, or NULL (0)
+  const int32_t* cu;            // [B + 1] row offsets of the requests
+  int32_t B;
+  int64_t total;
+  uint8_t* out_codes;
+  float* out_scale;
+  void* out_values;
+  WsHeader* hdr;
+};
+dsa_status launch_cache_read(const ReadParams& p, int values, cudaStream_t stream);
+
+// Latent attention, absorbed (decode) and expanded (prefill) forms.
+struct LatentDecodeParams {
+  const void* q;
+  int64_t qs_t, qs_h;
+  const void* latent;
+  int32_t n_blocks, block_size;
+  const int32_t* block_table;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  int32_t B, q_len, Hq;
+  float scale;
+  void* out;
+  float* lse;
+  WsHeader* hdr;
+  uint64_t budget_ns;
+  int num_sms;
+};
+size_t latent_decode_workspace_bytes(int B, int q_len, int Hq);
+dsa_status launch_latent_decode(const LatentDecodeParams& p, int dtype, cudaStream_t stream);
+struct LatentPrefillParams {
+  const void* q;
+  int64_t qs_t, qs_h;
+  const void* k_nope;
+  int64_t ks_t, ks_h;
+  const void* k_pe;
+  int64_t pes_t;
+  const void* v;
+  int64_t vs_t, vs_h;
+  const int32_t *cu_q, *cu_k;
+  int32_t B, Tq, Tk, max_q, H, causal;
+  float scale;
+  void* out;
+  float* lse;
+  WsHeader* hdr;
+  uint64_t budget_ns;
+  int num_sms;
+};
+dsa_status launch_latent_prefill(const LatentPrefillParams& p, int dtype, cudaStream_t stream);
 dsa_status launch_overlap(const int32_t* const* layer_idx, int32_t n_layers, int32_t rows,
                           int32_t topk, int32_t n_keys, uint64_t* out_counts, uint64_t* out_valid,
                           double* out_overlap, void* ws, cudaStream_t stream, int num_sms);
