@@ -1,5 +1,6 @@
 // C-ABI entry points: host-side validation, workspace sizing, tensor-map encoding, the
 // IndexCache layer driver and device-status reporting. No device memory is allocated here.
+#include <atomic>
 #include <cstdlib>
 #include <cstring>
 #include <cudaTypedefs.h>
@@ -89,17 +90,26 @@ dsa_status check_quantise(const void* x, int64_t xs_t, int64_t xs_h, int64_t T, 
 
 }  // namespace
 
-bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
-                       uint32_t box_rows, uint64_t row_stride) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+// The driver's tensor-map encoder, looked up once (threads that meet here first look it up twice).
+static PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> found{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = found.load();
   if (!encode) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult qres;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &qres) != cudaSuccess ||
         qres != cudaDriverEntryPointSuccess || !fn)
-      return false;
+      return nullptr;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    found.store(encode);
   }
+  return encode;
+}
+
+bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
+                       uint32_t box_rows, uint64_t row_stride) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
   const cuuint64_t dims[2] = {row_bytes, rows};
   const cuuint64_t strides[1] = {row_stride ? row_stride : row_bytes};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes), box_rows};
@@ -108,6 +118,19 @@ bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, u
       row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tmap_3d_16(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint64_t row_stride,
+                       uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_outer) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {d, rows, outer};
+  const cuuint64_t strides[2] = {row_stride * 2, outer_stride * 2};
+  const cuuint32_t box[3] = {box_d, 1, box_outer};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -64,53 +64,6 @@ struct AttSmem {
 };
 static_assert(kAttPvSlots * kAttPvSlotBytes <= kAttQkStages * 48 * 1024, "value slots exceed the stages");
 
-__host__ __device__ constexpr uint32_t make_idesc_bf16(uint32_t M, uint32_t N) {
-  return (1u << 4)                 // D format F32
-         | (1u << 7) | (1u << 10)  // A, B format BF16
-         | ((N >> 3) << 17)        // N / 8
-         | ((M >> 4) << 24);       // M / 16
-}
-constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B operand MN-major (N contiguous)
-
-// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle: rows of 64
-// contiguous MN elements (128 bytes), eight K rows per 1024-byte atom; sbo = bytes between
-// groups of eight K rows, lbo = bytes between 64-element MN column blocks.
-__device__ __forceinline__ uint64_t make_smem_desc_mn(uint32_t smem_addr, uint32_t lbo, uint32_t sbo) {
-  uint64_t desc = 0;
-  desc |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  desc |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  desc |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  desc |= 1ull << 46;  // descriptor version
-  desc |= 2ull << 61;  // 128-byte swizzle
-  return desc;
-}
-
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 16-byte cp.async; src_bytes = 0 fills the destination with zeros.
-__device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gsrc, uint32_t src_bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem_dst)), "l"(gsrc),
-               "r"(src_bytes)
-               : "memory");
-}
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// Byte offset of 16-byte unit u of row r in a K-major tile of 128-byte rows with the 128-byte
-// swizzle (eight rows per 1024-byte atom, unit index XOR row index).
-__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t u) {
-  return (r >> 3) * 1024u + (r & 7u) * 128u + ((u ^ (r & 7u)) << 4);
-}
-
 struct AttParams {
   const uint16_t* q;          // [B][128][576] bf16
   const uint16_t* latent;     // [n_blocks * block_size][576] bf16

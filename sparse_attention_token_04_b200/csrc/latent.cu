@@ -71,39 +71,6 @@ __global__ void __launch_bounds__(256) latent_decode_plain_kernel(const LatentDe
   st.store(static_cast<T*>(p.out) + row * 512, p.lse ? p.lse + row : nullptr, lane);
 }
 
-template <int DT>
-__global__ void __launch_bounds__(256) latent_prefill_plain_kernel(const LatentPrefillParams p) {
-  using T = typename Elem<DT>::T;
-  const int lane = threadIdx.x & 31, b = blockIdx.z, h = blockIdx.y;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk || q1 - q0 > p.max_q) {
-    if (threadIdx.x == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SEQ_LEN);
-    return;
-  }
-  if (i >= q1 - q0) return;
-  const int sees = p.causal ? (k1 - k0) - (q1 - q0) + 1 + i : k1 - k0;
-  RowState<DT, 192, 128> st;
-  const T* q = static_cast<const T*>(p.q) + (q0 + i) * p.qs_t + h * p.qs_h;
-#pragma unroll
-  for (int e = 0; e < 6; ++e) st.q[e] = Elem<DT>::get(q[lane + 32 * e]);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) st.o[e] = 0.0f;
-  for (int s = k0; s < k0 + sees; ++s) {
-    const T* kn = static_cast<const T*>(p.k_nope) + s * p.ks_t + h * p.ks_h;
-    const T* pe = static_cast<const T*>(p.k_pe) + s * p.pes_t;
-    const T* vv = static_cast<const T*>(p.v) + s * p.vs_t + h * p.vs_h;
-    float kv[6], v[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) kv[e] = Elem<DT>::get(kn[lane + 32 * e]), v[e] = Elem<DT>::get(vv[lane + 32 * e]);
-    kv[4] = Elem<DT>::get(pe[lane]);
-    kv[5] = Elem<DT>::get(pe[lane + 32]);
-    st.step(kv, v, p.scale);
-  }
-  const int64_t row = static_cast<int64_t>(q0 + i) * p.H + h;
-  st.store(static_cast<T*>(p.out) + row * 128, p.lse ? p.lse + row : nullptr, lane);
-}
-
 size_t latent_decode_workspace_bytes(int B, int q_len, int Hq) {
   (void)B, (void)q_len, (void)Hq;
   return DSA_WS_HEADER_BYTES;
@@ -114,13 +81,6 @@ dsa_status launch_latent_decode(const LatentDecodeParams& p, int dtype, cudaStre
   const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
   if (dtype == DSA_DTYPE_BF16) latent_decode_plain_kernel<DSA_DTYPE_BF16><<<grid, 256, 0, stream>>>(p);
   else latent_decode_plain_kernel<DSA_DTYPE_F16><<<grid, 256, 0, stream>>>(p);
-  return cuda_status(cudaGetLastError());
-}
-
-dsa_status launch_latent_prefill(const LatentPrefillParams& p, int dtype, cudaStream_t stream) {
-  const dim3 grid((p.max_q + 7) / 8, p.H, p.B);
-  if (dtype == DSA_DTYPE_BF16) latent_prefill_plain_kernel<DSA_DTYPE_BF16><<<grid, 256, 0, stream>>>(p);
-  else latent_prefill_plain_kernel<DSA_DTYPE_F16><<<grid, 256, 0, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
 

@@ -1,0 +1,382 @@
+// Latent attention of ragged prefills (expanded form) for sm_100a: out = softmax(scale Q K^T) V per
+// head, K = (k_nope | k_pe) 192 wide, V 128 wide, causal or not.
+//
+// A CTA takes 256 queries of one head as two 128-row tiles and walks the request's keys 128 at a
+// time. Per key tile and query tile: S = Q K^T (128 x 128 x 192) into TMEM, the softmax of S by 128
+// threads (thread = row), P = exp(S - m) back into TMEM over S's columns as 16-bit pairs, and
+// O += P V (128 x 128 x 128) with P read from TMEM. The two query tiles alternate: the tensor core
+// works for one while the other's softmax runs.
+//   warps 0-3, 4-7  softmax of query tile 0, 1: running maximum m and sum l of the row, O rescaled
+//                   in TMEM only when m has grown by more than 2^kLazy (so that the accumulator is
+//                   touched a few times per row, not every tile); at the end O / l and lse;
+//   warp 8          TMA: the query tiles once, K tiles two deep, V tiles one deep (a V tile's
+//                   successor is needed two S products after it is released);
+//   warp 9          one thread issues every MMA, in the order PV(0, j), QK(0, j+1), PV(1, j),
+//                   QK(1, j+1). QK(w, j+1) overwrites the columns that PV(w, j) reads P from: both go
+//                   down the one tensor pipe in issue order.
+// Shared memory: 96 KB of Q, 96 KB of K, 32 KB of V, all [128 rows][64 dims] blocks with the 128-byte
+// swizzle. TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and 384-511.
+//
+// Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
+// take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dsa {
+
+constexpr int kLpTile = 128;                 // query rows of a tile, keys of a tile
+constexpr int kLpThreads = 320;
+constexpr int kLpBlock = kLpTile * 128;      // 16 KB: 128 rows x 64 dims
+constexpr int kLpKStages = 2;
+constexpr float kLpLazy = 6.0f;              // log2 growth of a row's maximum that is left unscaled
+
+struct LpSmem {
+  uint8_t q[2][3][kLpBlock];
+  uint8_t k[kLpKStages][3][kLpBlock];
+  uint8_t v[2][kLpBlock];
+  uint64_t q_full[2], k_full[kLpKStages], k_empty[kLpKStages], v_full, v_empty;
+  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+struct LpParams {
+  const int32_t *cu_q, *cu_k;
+  int32_t Tq, Tk, max_q, H, causal;
+  float scale, scale_log2;
+  void* out;
+  float* lse;
+  WsHeader* hdr;
+  uint64_t budget_ns;
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
+  if constexpr (DT == DSA_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads, 1)
+    latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                          const __grid_constant__ CUtensorMap map_pe, const __grid_constant__ CUtensorMap map_v,
+                          const LpParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  LpSmem& sm = *reinterpret_cast<LpSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                          ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x, b = blockIdx.z;
+  const int qb = gridDim.y - 1 - blockIdx.y;  // the longest rows of a causal call first
+
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+  if (q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk || q1 - q0 > p.max_q) {
+    if (tid == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SEQ_LEN);
+    return;
+  }
+  const int nq = q1 - q0, nk = k1 - k0, i0 = qb * 2 * kLpTile;
+  if (i0 >= nq) return;
+  // Keys that query i of the request sees, and the key tiles of each query tile.
+  auto sees = [&](int i) { return p.causal ? max(0, min(nk, nk - nq + 1 + i)) : nk; };
+  int nt[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const int first = i0 + w * kLpTile, last = min(first + kLpTile, nq) - 1;
+    nt[w] = first < nq ? (sees(last) + kLpTile - 1) / kLpTile : 0;
+  }
+  const int n_tiles = max(nt[0], nt[1]);
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.o_done[i], 1);
+    }
+    for (int i = 0; i < kLpKStages; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    mbar_init(&sm.v_full, 1);
+    mbar_init(&sm.v_empty, 1);
+    mbar_init(&sm.drain, 1);
+    fence_mbar_init();
+    sm.abort = 0;
+  }
+  if (warp == 9) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+  const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
+
+  if (warp == 8) {
+    if (lane == 0) {
+      auto load_q = [&](int w) {
+        mbar_arrive_expect_tx(&sm.q_full[w], 3 * kLpBlock);
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(sm.q[w][c], &map_q, c * 64, h, q0 + i0 + w * kLpTile, &sm.q_full[w]);
+      };
+      auto load_k = [&](int j) {
+        const int st = j % kLpKStages;
+        if (!mbar_wait(&sm.k_empty[st], ((j / kLpKStages) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
+        mbar_arrive_expect_tx(&sm.k_full[st], 3 * kLpBlock);
+        for (int c = 0; c < 2; ++c) tma_load_3d(sm.k[st][c], &map_k, c * 64, h, k0 + j * kLpTile, &sm.k_full[st]);
+        tma_load_3d(sm.k[st][2], &map_pe, 0, 0, k0 + j * kLpTile, &sm.k_full[st]);
+        return true;
+      };
+      auto load_v = [&](int j) {
+        if (!mbar_wait(&sm.v_empty, (j & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
+        mbar_arrive_expect_tx(&sm.v_full, 2 * kLpBlock);
+        for (int c = 0; c < 2; ++c) tma_load_3d(sm.v[c], &map_v, c * 64, h, k0 + j * kLpTile, &sm.v_full);
+        return true;
+      };
+      int nk_issued = 0, nv_issued = 0;
+      if (n_tiles > 0) {
+        if (nt[0] > 0) load_q(0);
+        if (load_k(0)) ++nk_issued;
+        if (nt[1] > 0) load_q(1);
+        for (int j = 0; j < n_tiles; ++j) {
+          // K tile j + 1 is released (by the S products of tile j - 1) before V tile j is (by PV j - 1)
+          if (j + 1 < n_tiles) {
+            if (!load_k(j + 1)) break;
+            ++nk_issued;
+          }
+          if (!load_v(j)) break;
+          ++nv_issued;
+        }
+        // Let every copy land before the CTA exits (bounded).
+        for (int w = 0; w < 2; ++w)
+          if (nt[w] > 0) mbar_wait_drain(&sm.q_full[w], 0, p.budget_ns);
+        for (int st = 0; st < kLpKStages; ++st) {
+          const int n = (nk_issued - st + kLpKStages - 1) / kLpKStages;
+          if (n > 0) mbar_wait_drain(&sm.k_full[st], (n - 1) & 1, p.budget_ns);
+        }
+        if (nv_issued > 0) mbar_wait_drain(&sm.v_full, (nv_issued - 1) & 1, p.budget_ns);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && n_tiles > 0) {
+      constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
+      constexpr uint32_t idesc_qk = make_idesc_16(bf16, kLpTile, kLpTile);
+      constexpr uint32_t idesc_pv = make_idesc_16(bf16, kLpTile, 128) | kIdescBMnMajor;
+      auto qk = [&](int w, int j) {
+        const int st = j % kLpKStages;
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t da = make_smem_desc(smem_u32(sm.q[w][c]), 128);
+          const uint64_t db = make_smem_desc(smem_u32(sm.k[st][c]), 128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(tmem + w * 128, da + 2ull * kk, db + 2ull * kk, idesc_qk, (c > 0 || kk > 0) ? 1u : 0u);
+        }
+        tc_commit(&sm.s_full[w]);
+      };
+      auto pv = [&](int w, int j) {
+        const uint32_t vb = smem_u32(sm.v[0]);
+#pragma unroll
+        for (int kk = 0; kk < kLpTile / 16; ++kk)
+          tc_mma_16_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, make_smem_desc_mn(vb + kk * 2048, kLpBlock, 1024),
+                       idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(&sm.o_done[w]);
+      };
+      bool ok = mbar_wait(&sm.k_full[0], 0, ctl, DETAIL_WAIT_KFULL);
+      for (int w = 0; w < 2 && ok; ++w) {
+        if (nt[w] == 0) continue;
+        ok = mbar_wait(&sm.q_full[w], 0, ctl, DETAIL_WAIT_QFULL);
+        if (!ok) break;
+        tc_fence_after();
+        qk(w, 0);
+      }
+      if (ok) tc_commit(&sm.k_empty[0]);
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        const int last = j < nt[1] ? 1 : 0;  // the query tile whose PV is the last of this key tile
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (j < nt[w]) {
+            ok = mbar_wait(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL) &&
+                 mbar_wait(&sm.p_ready[w], j & 1, ctl, DETAIL_WAIT_SCORES);
+            if (!ok) break;
+            tc_fence_after();
+            pv(w, j);
+            if (w == last) tc_commit(&sm.v_empty);
+          }
+          if (j + 1 < nt[w]) {
+            ok = mbar_wait(&sm.k_full[(j + 1) % kLpKStages], ((j + 1) / kLpKStages) & 1, ctl, DETAIL_WAIT_KFULL);
+            if (!ok) break;
+            tc_fence_after();
+            qk(w, j + 1);
+          }
+        }
+        if (ok && j + 1 < n_tiles) tc_commit(&sm.k_empty[(j + 1) % kLpKStages]);
+      }
+      tc_commit(&sm.drain);
+      mbar_wait_drain(&sm.drain, 0, p.budget_ns);
+    }
+    __syncwarp();
+  } else {
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane, first = i0 + w * kLpTile + (warp & 3) * 32, i = first + lane;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * 128 + lanes;
+    const int n_row = sees(i), n_warp = sees(first);
+    // In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
+    // are 2^-32 of the largest (and the largest, 2^(8 + kLpLazy), stays far inside its range).
+    constexpr float kShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < nt[w]; ++j) {
+      ok = mbar_wait(&sm.s_full[w], j & 1, ctl, DETAIL_WAIT_ACCFULL);
+      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      tc_fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, s[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
+      if ((j + 1) * kLpTile > n_warp) {
+        const int left = n_row - j * kLpTile;  // visible keys of this tile
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= left) s[c][e] = 0xFF800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[c][e]));
+      const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+      if (j == 0) {
+        m = mn;
+      } else if (__any_sync(0xFFFFFFFFu, (mn - m) * p.scale_log2 > kLpLazy)) {
+        // (-inf - -inf is NaN and compares false; the row's O is 0 then and stays so)
+        ok = mbar_wait(&sm.o_done[w], (j - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        tc_fence_after();
+        const float f = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * p.scale_log2);
+        m = mn;
+        l *= f;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(tO + c * 32, o);
+          tmem_wait_ld_regs(o);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st_32x32b_x32(tO + c * 32, o);
+        }
+        tmem_wait_st();
+      }
+      const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < 4; c += 2) {
+        uint32_t packed[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const float p0 = exp2_fast(fmaf(__uint_as_float(s[c + (e >> 5)][e & 31]), p.scale_log2, base));
+          const float p1 = exp2_fast(fmaf(__uint_as_float(s[c + (e >> 5)][(e & 31) + 1]), p.scale_log2, base));
+          sum[e & 2] += p0;
+          sum[(e & 2) + 1] += p1;
+          packed[e >> 1] = pack_16<DT>(p0, p1);
+        }
+        tmem_st_32x32b_x32(tS + c * 16, packed);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if ((j + 1) * kLpTile > nk) {
+        // Rows of V behind the request's last key belong to others: zero weights must meet zeros.
+        ok = mbar_wait(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL);
+        if (ok && row >= nk - j * kLpTile)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sm.v[c] + row * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.p_ready[w]);
+    }
+    if (ok && nt[w] > 0) ok = mbar_wait(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    tc_fence_after();
+    if (ok && first < nq) {
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      const int64_t at = static_cast<int64_t>(q0 + i) * p.H + h;
+      uint16_t* o_row = static_cast<uint16_t*>(p.out) + at * 128;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (nt[w] > 0) {
+          tmem_ld_32x32b_x32(tO + c * 32, o);
+          tmem_wait_ld_regs(o);
+        }
+        if (i < nq) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t r[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              r[u] = l > 0.0f ? pack_16<DT>(__uint_as_float(o[e + 2 * u]) * inv, __uint_as_float(o[e + 2 * u + 1]) * inv)
+                              : 0u;
+            *reinterpret_cast<uint4*>(o_row + c * 32 + e) = make_uint4(r[0], r[1], r[2], r[3]);
+          }
+        }
+      }
+      if (i < nq && p.lse)
+        p.lse[at] = l > 0.0f ? m * p.scale + (logf(l) - kShift * 0.69314718055994531f) : -INFINITY;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DT>
+static dsa_status launch_prefill_dt(const LatentPrefillParams& a, cudaStream_t stream) {
+  CUtensorMap mq, mk, mpe, mv;
+  // With no keys at all no key box is loaded: any valid map does.
+  const bool none = a.Tk == 0;
+  const uint64_t Tk = none ? 1 : a.Tk;
+  if (!encode_tmap_3d_16(&mq, a.q, 192, a.H, a.qs_h, a.Tq, a.qs_t, 64, kLpTile) ||
+      !encode_tmap_3d_16(&mk, none ? a.q : a.k_nope, 128, a.H, a.ks_h, Tk, a.ks_t, 64, kLpTile) ||
+      !encode_tmap_3d_16(&mpe, none ? a.q : a.k_pe, 64, 1, 64, Tk, a.pes_t, 64, kLpTile) ||
+      !encode_tmap_3d_16(&mv, none ? a.q : a.v, 128, a.H, a.vs_h, Tk, a.vs_t, 64, kLpTile))
+    return DSA_ERR_CUDA;
+  const LpParams p{a.cu_q, a.cu_k, a.Tq, a.Tk, a.max_q, a.H, a.causal, a.scale, a.scale * 1.4426950408889634f,
+                   a.out, a.lse, a.hdr, a.budget_ns};
+  const size_t smem = sizeof(LpSmem) + 1024;
+  static_assert(sizeof(LpSmem) + 1024 <= 227 * 1024, "shared memory");
+  if (cudaFuncSetAttribute(latent_prefill_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const dim3 grid(a.H, (a.max_q + 2 * kLpTile - 1) / (2 * kLpTile), a.B);
+  latent_prefill_kernel<DT><<<grid, kLpThreads, smem, stream>>>(mq, mk, mpe, mv, p);
+  return cuda_status(cudaGetLastError());
+}
+
+dsa_status launch_latent_prefill(const LatentPrefillParams& a, int dtype, cudaStream_t stream) {
+  return dtype == DSA_DTYPE_BF16 ? launch_prefill_dt<DSA_DTYPE_BF16>(a, stream)
+                                 : launch_prefill_dt<DSA_DTYPE_F16>(a, stream);
+}
+
+}  // namespace dsa
