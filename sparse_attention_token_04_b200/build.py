@@ -21,7 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG, "libdsa_indexer.so")
 SOURCES = ["api.cu", "prefill.cu", "decode.cu", "topk.cu", "overlap.cu", "selftest.cu", "noalloc.cu", "merge.cu", "pattern.cu", "attention.cu",
-           "rotary.cu", "index_cache.cu", "latent.cu", "latent_prefill.cu"]
+           "rotary.cu", "index_cache.cu", "latent_decode.cu", "latent_prefill.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                 "-I", INCLUDE]

@@ -345,7 +345,9 @@ DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_s
 
 DSA_API size_t dsa_latent_attention_decode_workspace_bytes(int32_t B, int32_t q_len, int32_t Hq) {
   if (B < 1 || B > DSA_DECODE_MAX_REQUESTS || q_len < 1 || q_len > 8 || Hq < 1 || Hq > 128) return 0;
-  return latent_decode_workspace_bytes(B, q_len, Hq);
+  const int sms = current_num_sms();
+  if (sms < 1) return 0;
+  return latent_decode_workspace_bytes(B, q_len, Hq, sms);
 }
 
 DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t, int64_t q_stride_h,
@@ -366,9 +368,9 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
       Hq > 128 || block_size % 8 || B > DSA_DECODE_MAX_REQUESTS)
     return DSA_ERR_UNSUPPORTED;
   if (!workspace || !aligned(workspace, 256)) return DSA_ERR_INVALID;
-  if (workspace_bytes < latent_decode_workspace_bytes(B, q_len, Hq)) return DSA_ERR_INVALID;
   const int sms = current_num_sms();
   if (sms < 1) return DSA_ERR_CUDA;
+  if (workspace_bytes < latent_decode_workspace_bytes(B, q_len, Hq, sms)) return DSA_ERR_INVALID;
   const LatentDecodeParams p{q, q_stride_t, q_stride_h, latent, n_blocks, block_size, block_table,
                              max_blocks, seq_lens, B, q_len, Hq, scale, out, lse,
                              static_cast<WsHeader*>(workspace), wait_budget_ns(), sms};

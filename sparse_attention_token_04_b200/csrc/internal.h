@@ -224,7 +224,7 @@ struct LatentDecodeParams {
   uint64_t budget_ns;
   int num_sms;
 };
-size_t latent_decode_workspace_bytes(int B, int q_len, int Hq);
+size_t latent_decode_workspace_bytes(int B, int q_len, int Hq, int num_sms);
 dsa_status launch_latent_decode(const LatentDecodeParams& p, int dtype, cudaStream_t stream);
 struct LatentPrefillParams {
   const void* q;

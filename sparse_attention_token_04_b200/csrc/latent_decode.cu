@@ -1,0 +1,635 @@
+// Dense latent attention of decode queries (absorbed form) for sm_100a: 1 to 8 new tokens a request
+// against all of the request's paged 576-wide latents, whose first 512 entries are the values.
+//
+// A request's query rows are its q_len * Hq (token, head) pairs, taken HT (16, 32 or 64) at a time.
+// For one row tile the requests' key tiles (64 keys each), laid end to end, are split into equal
+// contiguous ranges, one per CTA, so that every CTA streams the same number of tiles whatever the
+// lengths; the part of a range inside one request is a segment. A segment that is a whole request
+// writes its outputs, any other its unnormalised sums with m and l, and latent_combine_kernel joins
+// those of a request. The grid is one CTA per SM over all row tiles, so row tiles of the same
+// request run side by side and the second one finds the latents in L2.
+//
+// Per key tile: S = Q K^T (rows x 64 keys x 576) into TMEM, softmax numerators P to shared memory,
+// and O^T += V^T P^T (4 x 128 dims x rows x 64 keys). The latent tile in shared memory serves both
+// products: as K (dims contiguous, K-major) and as V^T (the same bytes, M-major), so every latent is
+// fetched once. O^T has the dims on TMEM lanes and the rows on columns: 4 * HT columns, which is what
+// leaves room beside it (512 dims of 64 rows in 32 bits are half of TMEM).
+//   warps 0-3  the queries of each segment into shared memory; softmax (thread = row, warps 0 and 1
+//              at most); O^T rescaled (thread = dim) only when some row's maximum has grown by more
+//              than 2^kLdLazy; the segment's outputs;
+//   warp 4     TMA: nine 64-dim chunks of 8 KB a tile, the last chunk of the latent first (it is only
+//              a key and is released first), into a ring of 18 (two tiles);
+//   warp 5     one thread issues the MMAs: a tile's PV as soon as its P is there, else the next QK
+//              chunk that has landed.
+// Bound by HBM for up to 64 rows a request (1152 B a key); with 128 rows the products (278528 FLOP a
+// key) take as long as the bytes.
+#include <algorithm>
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dsa {
+
+constexpr int kLdDqk = 576, kLdDv = 512;
+constexpr int kLdKeys = 64;                     // keys of a tile
+constexpr int kLdChunks = kLdDqk / 64;          // 9
+constexpr int kLdSlots = 2 * kLdChunks;         // a tile's value chunks never wrap around the ring
+constexpr int kLdSlotBytes = kLdKeys * 128;     // 8 KB
+constexpr int kLdThreads = 192;
+constexpr float kLdLazy = 6.0f;
+
+template <int HT>
+struct LdSmem {
+  uint8_t q[kLdChunks][HT * 128];               // the MMA reads 128 rows from each: into what follows
+  uint8_t p[HT * 128];
+  uint8_t ring[kLdSlots][kLdSlotBytes];
+  float fac[HT];
+  uint64_t full[kLdSlots], empty[kLdSlots];
+  uint64_t q_full, s_full[2], p_ready, pv_done, drain;
+  uint32_t tmem;
+  int abort;
+  int b0, tile0, ntiles;                        // this CTA's range
+};
+
+struct LdParams {
+  const uint16_t* q;
+  int64_t qs_t, qs_h;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t n_blocks, block_size, max_blocks, B, q_len, Hq;
+  int32_t box_rows;                             // latent rows of one TMA box
+  float scale, scale_log2;
+  uint16_t* out;
+  float* lse;
+  float* part;                                  // [row tiles][CTAs][2][512][HT] unnormalised O^T
+  float* ml;                                    // [row tiles][CTAs][2][2][HT] m, l
+  WsHeader* hdr;
+  uint64_t budget_ns;
+};
+
+__device__ __forceinline__ int ld_len(const LdParams& p, int b) {
+  return max(0, min(__ldg(&p.seq_lens[b]), p.max_blocks * p.block_size));
+}
+__device__ __forceinline__ int ld_tiles(const LdParams& p, int b) { return (ld_len(p, b) + kLdKeys - 1) / kLdKeys; }
+
+// Key tiles of requests [0, n), by one warp.
+__device__ __forceinline__ int64_t ld_tiles_before(const LdParams& p, int n, int lane) {
+  int64_t sum = 0;
+  for (int b = lane; b < n; b += 32) sum += ld_tiles(p, b);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+  return sum;
+}
+
+// CTAs of a row tile that share T key tiles: no more than there are tiles, so that each has some.
+__device__ __forceinline__ int64_t ld_sharers(int64_t T, int n_cta) { return T < n_cta ? (T > 0 ? T : 1) : n_cta; }
+
+template <int DT>
+__device__ __forceinline__ uint32_t ld_pack(float lo, float hi) {
+  if constexpr (DT == DSA_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint16_t ld_round(float x) {
+  return static_cast<uint16_t>(ld_pack<DT>(x, 0.0f));
+}
+
+// In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
+// are 2^-32 of the largest (and the largest, 2^(8 + kLdLazy), stays far inside its range).
+template <int DT>
+constexpr float kLdShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
+
+template <int CW>
+__device__ __forceinline__ void ld_columns(uint32_t taddr, uint32_t (&r)[CW]) {
+  if constexpr (CW == 32) {
+    tmem_ld_32x32b_x32(taddr, r);
+    tmem_wait_ld_regs(r);
+  } else {
+    tmem_ld_32x32b_x16(taddr, r);
+    tmem_wait_ld_regs16(r);
+  }
+}
+
+template <int DT, int HT>
+__global__ void __launch_bounds__(kLdThreads, 1)
+    latent_decode_kernel(const __grid_constant__ CUtensorMap map_latent, const LdParams p) {
+  constexpr int CW = HT < 32 ? HT : 32;         // TMEM columns read at a time
+  extern __shared__ uint8_t smem_raw[];
+  LdSmem<HT>& sm = *reinterpret_cast<LdSmem<HT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                  ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ht = blockIdx.x, cta = blockIdx.y;  // row tiles fastest: those of one range run together
+  const int R = p.q_len * p.Hq;
+
+  if (tid == 0) {
+    for (int i = 0; i < kLdSlots; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
+    }
+    mbar_init(&sm.q_full, 4);
+    mbar_init(&sm.s_full[0], 1);
+    mbar_init(&sm.s_full[1], 1);
+    mbar_init(&sm.p_ready, 4);
+    mbar_init(&sm.pv_done, 1);
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    // This CTA's range [lo, hi) of all key tiles, and the request holding lo.
+    if (cta == 0 && ht == 0)
+      for (int b = lane; b < p.B; b += 32) {
+        const int n = __ldg(&p.seq_lens[b]);
+        if (n < 0 || n > p.max_blocks * p.block_size) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SEQ_LEN);
+      }
+    const int64_t T = ld_tiles_before(p, p.B, lane);
+    const int64_t G = ld_sharers(T, gridDim.y);
+    const int64_t lo = cta < G ? T * cta / G : T, hi = cta < G ? T * (cta + 1) / G : T;
+    int64_t carry = 0;
+    for (int base = 0; base < p.B && lo < hi; base += 32) {
+      const int bb = base + lane;
+      const int nt = bb < p.B ? ld_tiles(p, bb) : 0;
+      int incl = nt;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      const int64_t start = carry + incl - nt;
+      if (start <= lo && lo < start + nt) {
+        sm.b0 = bb;
+        sm.tile0 = static_cast<int>(lo - start);
+      }
+      carry += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (carry > lo) break;
+    }
+    if (lane == 0) sm.ntiles = static_cast<int>(hi - lo);
+  }
+  if (warp == 5) {
+    tmem_alloc(&sm.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem, tO = tmem + 128;
+  const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
+  const int total = sm.ntiles;
+
+  if (warp == 4) {
+    if (lane == 0 && total > 0) {
+      const int n_box = kLdKeys / p.box_rows;
+      // First latent row of each box of request b's key tile t (-1: at or behind the request's end).
+      auto box_rows = [&](int b, int t, int n, int (&rows)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int s = t * kLdKeys + i * p.box_rows;
+          rows[i] = -1;
+          if (i < n_box && s < n) {
+            int blk = __ldg(&p.block_table[static_cast<int64_t>(b) * p.max_blocks + s / p.block_size]);
+            if (blk < 0 || blk >= p.n_blocks) {
+              record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_BLOCK_TABLE);
+              blk = 0;
+            }
+            rows[i] = blk * p.block_size + s % p.block_size;
+          }
+        }
+      };
+      int b = sm.b0, t = sm.tile0, left = total;
+      int n = ld_len(p, b), rows[8];
+      box_rows(b, t, n, rows);
+      uint32_t g = 0;                           // chunks issued
+      bool ok = true;
+      while (left > 0 && ok) {
+        int cur[8], bytes = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cur[i] = rows[i];
+          if (cur[i] >= 0) bytes += p.box_rows * 128;
+        }
+        if (--left > 0) {                       // the next tile's table entries, a tile ahead
+          if (++t >= (n + kLdKeys - 1) / kLdKeys) {
+            t = 0;
+            do n = ld_len(p, ++b);
+            while (n == 0);
+          }
+          box_rows(b, t, n, rows);
+        }
+        for (int c = 0; c < kLdChunks; ++c, ++g) {
+          const uint32_t s = g % kLdSlots;
+          ok = mbar_wait(&sm.empty[s], ((g / kLdSlots) & 1u) ^ 1u, ctl, DETAIL_WAIT_KEMPTY);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&sm.full[s], bytes);
+          const int x = c == 0 ? kLdDv : (c - 1) * 64;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (cur[i] >= 0) tma_load_3d(sm.ring[s] + i * p.box_rows * 128, &map_latent, x, 0, cur[i], &sm.full[s]);
+        }
+      }
+      // Let every copy land before the CTA exits (bounded).
+      for (uint32_t s = 0; s < kLdSlots; ++s)
+        if (g > s) mbar_wait_drain(&sm.full[s], ((g - s - 1) / kLdSlots) & 1u, p.budget_ns);
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    if (lane == 0 && total > 0) {
+      constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
+      constexpr uint32_t idesc_qk = make_idesc_16(bf16, 128, kLdKeys);
+      constexpr uint32_t idesc_pv = make_idesc_16(bf16, 128, HT) | kIdescAMnMajor;
+      // Tiles of the segment that QK and PV are in, and their tiles so far.
+      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, chunk = 0;
+      int vb = qb, v_left = q_left, pv = 0;
+      bool v_first = true, q_seen = false;
+      uint64_t since = 0;
+      bool ok = true;
+      while (pv < total) {
+        bool moved = false;
+        if (pv < qk && mbar_try_wait(&sm.p_ready, pv & 1)) {
+          tc_fence_after();
+          const uint32_t s0 = (pv & 1) * kLdChunks + 1;  // first value slot of the tile
+          const uint64_t db = make_smem_desc(smem_u32(sm.p), 128);
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt) {
+            const uint32_t va = smem_u32(sm.ring[s0 + 2 * mt]);
+#pragma unroll
+            for (int kk = 0; kk < kLdKeys / 16; ++kk)
+              tc_mma_bf16(tO + mt * HT, make_smem_desc_mn(va + kk * 2048, kLdSlotBytes, 1024), db + 2ull * kk, idesc_pv,
+                          (!v_first || kk > 0) ? 1u : 0u);
+            tc_commit(&sm.empty[s0 + 2 * mt]);
+            tc_commit(&sm.empty[s0 + 2 * mt + 1]);
+          }
+          tc_commit(&sm.pv_done);
+          ++pv;
+          v_first = false;
+          if (--v_left == 0 && pv < total) {
+            do v_left = min(ld_tiles(p, ++vb), total - pv);
+            while (v_left == 0);
+            v_first = true;
+          }
+          moved = true;
+        } else if (qk < total && qk < pv + 2) {
+          // S[qk & 1] is free: the P of tile qk - 2 has been seen
+          if (!q_seen) q_seen = mbar_try_wait(&sm.q_full, q_seg & 1);
+          const uint32_t slot = (qk & 1) * kLdChunks + chunk;
+          if (q_seen && mbar_try_wait(&sm.full[slot], (qk >> 1) & 1)) {
+            tc_fence_after();
+            const uint64_t da = make_smem_desc(smem_u32(sm.q[chunk]), 128);
+            const uint64_t db = make_smem_desc(smem_u32(sm.ring[slot]), 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(tmem + (qk & 1) * kLdKeys, da + 2ull * kk, db + 2ull * kk, idesc_qk,
+                          (chunk > 0 || kk > 0) ? 1u : 0u);
+            if (chunk == 0) tc_commit(&sm.empty[slot]);
+            if (++chunk == kLdChunks) {
+              tc_commit(&sm.s_full[qk & 1]);
+              chunk = 0;
+              ++qk;
+              if (--q_left == 0 && qk < total) {
+                do q_left = min(ld_tiles(p, ++qb), total - qk);
+                while (q_left == 0);
+                ++q_seg;
+                q_seen = false;
+              }
+            }
+            moved = true;
+          }
+        }
+        if (moved) {
+          since = 0;
+        } else {
+          const uint64_t now = globaltimer_ns();
+          if (since == 0) since = now;
+          if (*ctl.abort) ok = false;
+          else if (now - since > p.budget_ns) {
+            *ctl.abort = 1;
+            record_error(p.hdr, DSA_ERR_TIMEOUT, DETAIL_WAIT_KFULL);
+            ok = false;
+          }
+          if (!ok) break;
+        }
+      }
+      tc_commit(&sm.drain);
+      mbar_wait_drain(&sm.drain, 0, p.budget_ns);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int row = warp * 32 + lane, r = ht * HT + row;  // row of the tile, of the request
+    const bool softmax_warp = warp * 32 < HT;
+    int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0;
+    bool ok = true;
+    for (; left > 0; ++b, t = 0) {
+      const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left);
+      if (te <= t) continue;
+      left -= te - t;
+      // The segment's queries (zeros behind the last row); the QK products of the segment before are
+      // done: this warp has seen their last S.
+      {
+        const uint16_t* qb = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
+        for (int u = tid; u < HT * kLdDqk / 8; u += 128) {
+          const int qr = u / (kLdDqk / 8), x = u % (kLdDqk / 8), rr = ht * HT + qr;
+          const int chunk = x >= kLdDv / 8 ? 0 : x / 8 + 1;
+          const uint16_t* src = rr < R ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h + x * 8 : qb;
+          cp_async_16(sm.q[chunk] + sw128(qr, x & 7), src, rr < R ? 16u : 0u);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full);
+        ++seg;
+      }
+      const int sees = r < R ? max(0, n - p.q_len + 1 + r / p.Hq) : n;
+      float m = -INFINITY, l = 0.0f;
+      const int t_first = t;
+      for (; t < te; ++t, ++done) {
+        ok = mbar_wait(&sm.s_full[done & 1], (done >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+        if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s[2][32];
+        float mn = m;
+        bool grow = false;
+        if (softmax_warp) {
+          const uint32_t tS = tmem + (done & 1) * kLdKeys + lanes;
+          tmem_ld_32x32b_x32(tS, s[0]);
+          tmem_ld_32x32b_x32(tS + 32, s[1]);
+          tmem_wait_ld_regs(s[0]);
+          tmem_wait_ld_regs(s[1]);
+          const int seen = sees - t * kLdKeys;  // visible keys of this tile
+          if (__any_sync(0xFFFFFFFFu, seen < kLdKeys)) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e)
+              if (e >= seen) s[e >> 5][e & 31] = 0xFF800000u;  // -inf
+          }
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e >> 5][e & 31]));
+          mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // (-inf - -inf is NaN and compares false)
+          grow = row < HT && t > t_first && (mn - m) * p.scale_log2 > kLdLazy;
+        }
+        // P's buffer is free, and O^T may be rescaled, once the PV of the tile before is done.
+        if (t > t_first) ok = mbar_wait(&sm.pv_done, (done - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+        if (t == t_first) m = mn;
+        if (named_bar_or(2, 128, grow)) {
+          if (softmax_warp) {
+            const float f = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * p.scale_log2);
+            m = mn;
+            l *= f;
+            if (row < HT) sm.fac[row] = f;
+          }
+          named_bar(3, 128);
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * HT; c += CW) {
+            uint32_t o[CW];
+            ld_columns<CW>(tO + lanes + c, o);
+#pragma unroll
+            for (int e = 0; e < CW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[(c & (HT - 1)) + e]);
+            if constexpr (CW == 32) tmem_st_32x32b_x32(tO + lanes + c, o);
+            else tmem_st_32x32b_x16(tO + lanes + c, o);
+          }
+          tmem_wait_st();
+        }
+        if (softmax_warp && row < HT) {
+          const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const int k = u * 8 + e;
+              const float p0 = exp2_fast(fmaf(__uint_as_float(s[k >> 5][k & 31]), p.scale_log2, base));
+              const float p1 = exp2_fast(fmaf(__uint_as_float(s[(k + 1) >> 5][(k + 1) & 31]), p.scale_log2, base));
+              sum[e & 2] += p0;
+              sum[(e & 2) + 1] += p1;
+              w4[e >> 1] = ld_pack<DT>(p0, p1);
+            }
+            *reinterpret_cast<uint4*>(sm.p + sw128(row, u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        if ((t + 1) * kLdKeys > n) {
+          // Rows behind the request's last key hold anything: zero weights must meet zeros.
+          const int key = tid >> 1;
+          if (key >= n - t * kLdKeys)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(sm.ring[(done & 1) * kLdChunks + 1 + 4 * (tid & 1) + c] + key * 128 + u * 16) =
+                    make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready);
+      }
+      if (!ok) break;
+      // The segment's result.
+      ok = mbar_wait(&sm.pv_done, (done - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+      const bool whole = t_first == 0 && te == nt;
+      if (softmax_warp && row < HT) {
+        if (whole) {
+          sm.fac[row] = l > 0.0f ? 1.0f / l : 0.0f;
+          if (p.lse && r < R)
+            p.lse[static_cast<int64_t>(b) * R + r] =
+                l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+        } else {
+          float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
+          ml[row] = m;
+          ml[HT + row] = l;
+        }
+      }
+      if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+      tc_fence_after();
+      float* part = p.part + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * kLdDv * HT;
+#pragma unroll 1
+      for (int c = 0; c < 4 * HT; c += CW) {
+        uint32_t o[CW];
+        ld_columns<CW>(tO + lanes + c, o);
+        const int dim = c / HT * 128 + row, h0 = c & (HT - 1);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < CW; ++e) {
+            const int rr = ht * HT + h0 + e;
+            if (rr < R)
+              p.out[(static_cast<int64_t>(b) * R + rr) * kLdDv + dim] =
+                  sm.fac[h0 + e] > 0.0f ? ld_round<DT>(__uint_as_float(o[e]) * sm.fac[h0 + e]) : static_cast<uint16_t>(0);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < CW; e += 4)
+            *reinterpret_cast<uint4*>(part + dim * HT + h0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+      tc_fence_before();
+      named_bar(1, 128);  // fac is read by all before the next segment writes it
+    }
+  }
+  __syncthreads();
+  grid_launch_dependents();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the split requests: with M the largest m_c of a row, out = sum_c 2^((m_c - M) scale log2 e) O_c
+// / L, L the same sum of the l_c, lse = scale M + ln L. A request without keys gets zeros and -inf.
+// Block (x, ht, z) takes 64 of the dims of a run of requests; the partial sums are read along the
+// rows (as they were written) and turned in shared memory so that out is written along the dims.
+constexpr int kLcDims = 64;
+template <int DT, int HT>
+__global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, int n_cta) {
+  extern __shared__ __align__(16) float lc_smem[];
+  float* wt = lc_smem;                          // [splits][HT]
+  float* tile = lc_smem + n_cta * HT;           // [HT][kLcDims + 1]
+  __shared__ int64_t sh[2];
+  const int tid = threadIdx.x, ht = blockIdx.y, d0 = blockIdx.z * kLcDims;
+  const int R = p.q_len * p.Hq, rows = min(HT, R - ht * HT);
+  const int b_lo = static_cast<int>(static_cast<int64_t>(p.B) * blockIdx.x / gridDim.x);
+  const int b_hi = static_cast<int>(static_cast<int64_t>(p.B) * (blockIdx.x + 1) / gridDim.x);
+  if (tid < 64) {
+    const int64_t n = ld_tiles_before(p, tid < 32 ? p.B : b_lo, tid & 31);
+    if ((tid & 31) == 0) sh[tid >> 5] = n;
+  }
+  __syncthreads();
+  const int64_t T = sh[0], G = ld_sharers(T, n_cta);
+  int64_t start = sh[1];
+  grid_dependency_wait();
+  for (int b = b_lo; b < b_hi; ++b) {
+    const int nt = ld_tiles(p, b);
+    const int64_t first = start;
+    start += nt;
+    uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT) * kLdDv + d0;
+    float* lse = p.lse ? p.lse + static_cast<int64_t>(b) * R + ht * HT : nullptr;
+    if (nt == 0) {
+      for (int i = tid; i < rows * kLcDims; i += 256) out[(i / kLcDims) * kLdDv + i % kLcDims] = 0;
+      if (lse && blockIdx.z == 0 && tid < rows) lse[tid] = -INFINITY;
+      continue;
+    }
+    // CTA c holds tiles [T c / G, T (c + 1) / G): the holder of tile x is ceil((x + 1) G / T) - 1.
+    const int c0 = static_cast<int>(((first + 1) * G - 1) / T), c1 = static_cast<int>(((first + nt) * G - 1) / T);
+    if (c0 == c1) continue;
+    const int ns = c1 - c0 + 1;
+    // The request's first CTA holds its beginning (slot 1), every other one begins inside it (slot 0).
+    auto slot = [&](int c) { return (static_cast<int64_t>(ht) * n_cta + c0 + c) * 2 + (c == 0 ? 1 : 0); };
+    if (tid < HT) {
+      float M = -INFINITY, L = 0.0f;
+      for (int c = 0; c < ns; ++c) M = fmaxf(M, p.ml[slot(c) * 2 * HT + tid]);
+      for (int c = 0; c < ns; ++c) {
+        const float mc = p.ml[slot(c) * 2 * HT + tid];
+        const float w = mc == -INFINITY ? 0.0f : exp2f((mc - M) * p.scale_log2);
+        wt[c * HT + tid] = w;
+        L += w * p.ml[slot(c) * 2 * HT + HT + tid];
+      }
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      for (int c = 0; c < ns; ++c) wt[c * HT + tid] *= inv;
+      if (lse && blockIdx.z == 0 && tid < rows)
+        lse[tid] = L > 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+    }
+    __syncthreads();
+    constexpr int kVecs = kLcDims * HT / 4;     // float4s of the block's dims
+#pragma unroll
+    for (int v = tid; v < kVecs; v += 256) {
+      const int dim = v / (HT / 4), h = v % (HT / 4) * 4;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int c = 0; c < ns; ++c) {
+        const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part + (slot(c) * kLdDv + d0 + dim) * HT + h));
+        const float4 w = *reinterpret_cast<const float4*>(wt + c * HT + h);
+        acc.x += w.x * o.x;
+        acc.y += w.y * o.y;
+        acc.z += w.z * o.z;
+        acc.w += w.w * o.w;
+      }
+      tile[(h + 0) * (kLcDims + 1) + dim] = acc.x;
+      tile[(h + 1) * (kLcDims + 1) + dim] = acc.y;
+      tile[(h + 2) * (kLcDims + 1) + dim] = acc.z;
+      tile[(h + 3) * (kLcDims + 1) + dim] = acc.w;
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * kLcDims / 2; i += 256) {
+      const int h = i / (kLcDims / 2), d = i % (kLcDims / 2) * 2;
+      *reinterpret_cast<uint32_t*>(out + h * kLdDv + d) =
+          ld_pack<DT>(tile[h * (kLcDims + 1) + d], tile[h * (kLcDims + 1) + d + 1]);
+    }
+    __syncthreads();
+  }
+}
+
+// Rows of a row tile: the fewest that take all rows of a request, 64 at most.
+static int ld_row_tile(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// CTAs of one row tile: all row tiles together fill the SMs once.
+static int ld_ctas(int row_tiles, int num_sms) { return std::max(1, num_sms / row_tiles); }
+
+size_t latent_decode_workspace_bytes(int B, int q_len, int Hq, int num_sms) {
+  (void)B;
+  const int rows = q_len * Hq, ht = ld_row_tile(rows), tiles = (rows + ht - 1) / ht;
+  const size_t segments = static_cast<size_t>(tiles) * ld_ctas(tiles, num_sms) * 2;
+  return DSA_WS_HEADER_BYTES + segments * ht * (kLdDv + 2) * sizeof(float);
+}
+
+template <int DT, int HT>
+static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t stream) {
+  const int R = a.q_len * a.Hq, row_tiles = (R + HT - 1) / HT, n_cta = ld_ctas(row_tiles, a.num_sms);
+  int box = kLdKeys;                            // the largest box that divides tiles and blocks
+  while (a.block_size % box) box /= 2;
+  CUtensorMap map;
+  if (!encode_tmap_3d_16(&map, a.latent, kLdDqk, 1, kLdDqk, static_cast<uint64_t>(a.n_blocks) * a.block_size, kLdDqk,
+                         64, box))
+    return DSA_ERR_CUDA;
+  float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.hdr) + DSA_WS_HEADER_BYTES);
+  const LdParams p{static_cast<const uint16_t*>(a.q), a.qs_t, a.qs_h, a.block_table, a.seq_lens, a.n_blocks,
+                   a.block_size, a.max_blocks, a.B, a.q_len, a.Hq, box, a.scale, a.scale * 1.4426950408889634f,
+                   static_cast<uint16_t*>(a.out), a.lse, part,
+                   part + static_cast<size_t>(row_tiles) * n_cta * 2 * kLdDv * HT, a.hdr, a.budget_ns};
+  const size_t smem = sizeof(LdSmem<HT>) + 1024;
+  static_assert(sizeof(LdSmem<HT>) + 1024 <= 227 * 1024, "shared memory");
+  const size_t csmem = (static_cast<size_t>(n_cta) * HT + HT * (kLcDims + 1)) * sizeof(float);
+  if (cudaFuncSetAttribute(latent_decode_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess ||
+      cudaFuncSetAttribute(latent_combine_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(csmem)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  latent_decode_kernel<DT, HT><<<dim3(row_tiles, n_cta), kLdThreads, smem, stream>>>(map, p);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(std::min(a.B, 128), row_tiles, kLdDv / kLcDims);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = csmem;
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, latent_combine_kernel<DT, HT>, p, n_cta));
+}
+
+template <int DT>
+static dsa_status launch_decode_dt(const LatentDecodeParams& a, cudaStream_t stream) {
+  switch (ld_row_tile(a.q_len * a.Hq)) {
+    case 16: return launch_decode_ht<DT, 16>(a, stream);
+    case 32: return launch_decode_ht<DT, 32>(a, stream);
+    default: return launch_decode_ht<DT, 64>(a, stream);
+  }
+}
+
+dsa_status launch_latent_decode(const LatentDecodeParams& a, int dtype, cudaStream_t stream) {
+  return dtype == DSA_DTYPE_BF16 ? launch_decode_dt<DSA_DTYPE_BF16>(a, stream)
+                                 : launch_decode_dt<DSA_DTYPE_F16>(a, stream);
+}
+
+}  // namespace dsa

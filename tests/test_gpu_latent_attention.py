@@ -114,6 +114,16 @@ def test_decode_many_requests_and_long_ones(B_, lo, hi, Hq):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
 
 
+def test_decode_fewer_tiles_than_sms_with_a_dirty_workspace():
+    """47 key tiles, fewer than there are SMs, with a workspace full of large numbers behind its header:
+    nothing is joined that the call has not written."""
+    q, latent, table, seq, scale = _decode_case([3000 - 129, 0, 129], 1, 16, 64, torch.bfloat16, 3)
+    ws = torch.full((B.dsa_latent_attention_decode_workspace_bytes(3, 1, 16),), 0x7E, dtype=torch.uint8, device="cuda")
+    B.dsa_workspace_init(ws)
+    out, lse = B.dsa_latent_attention_decode(q.cuda(), latent.cuda(), table.cuda(), seq.cuda(), scale, workspace=ws)
+    _check_decode(q, latent, table, seq, scale, 64, out, lse)
+
+
 def test_decode_strided_queries_and_no_lse():
     q, latent, table, seq, scale = _decode_case([100, 257], 2, 6, 64, torch.bfloat16, 5)
     wide = torch.full((4, 9, 600), float("nan"), dtype=torch.bfloat16)
