@@ -205,6 +205,63 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// Whether the phase with the given parity has completed, without suspending the thread (for a thread
+// that polls several barriers).
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// As mbar_wait, with everything but the first try out of line, for kernels whose roles hold a score of
+// waits: inlined, they are a large part of the code.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, WsHeader* hdr, volatile int* abort,
+                                            uint64_t budget_ns, uint32_t detail) {
+  uint64_t start = 0;
+  for (uint32_t i = 1;; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i & 15u) continue;  // the timer's read takes longer than most waits
+    if (abort && *abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (start == 0) start = now;
+    if (now - start > budget_ns) {
+      if (abort) {
+        *abort = 1;
+        record_error(hdr, DSA_ERR_TIMEOUT, detail);
+      }
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_call(uint64_t* bar, uint32_t parity, const WaitCtl& ctl, uint32_t detail) {
+  return mbar_try_wait(bar, parity) ||
+         mbar_wait_long(smem_u32(bar), parity, ctl.hdr, ctl.abort, ctl.budget_ns, detail);
+}
+// Bounded wait that ignores the abort flag (see mbar_wait_drain).
+__device__ __forceinline__ void mbar_drain_call(uint64_t* bar, uint32_t parity, uint64_t budget_ns) {
+  mbar_wait_long(smem_u32(bar), parity, nullptr, nullptr, budget_ns, 0);
+}
+// A whole warp's wait: one lane polls, the result is the same in all lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl& ctl, uint32_t detail) {
+  bool ok = true;
+  if (lane_id() == 0) ok = mbar_wait_call(bar, parity, ctl, detail);
+  return __shfl_sync(0xFFFFFFFFu, ok, 0);
+}
+
 // ------------------------------------------------------------------------------------------
 // TMA (every load fills only the issuing CTA's own shared memory)
 // ------------------------------------------------------------------------------------------

@@ -35,21 +35,23 @@
 namespace dsa {
 
 constexpr int kLdDqk = 576, kLdDv = 512;
-constexpr int kLdKeys = 64;                     // keys of a tile
+constexpr int kLdKeys = 32;                     // keys of a tile
 constexpr int kLdChunks = kLdDqk / 64;          // 9
-constexpr int kLdSlots = 2 * kLdChunks;         // a tile's value chunks never wrap around the ring
-constexpr int kLdSlotBytes = kLdKeys * 128;     // 8 KB
+constexpr int kLdGroups = 4;                    // barriers of a tile: chunks 0-2, 3-4, 5-6, 7-8
+constexpr int kLdSlotBytes = kLdKeys * 128;     // 4 KB: one chunk
+constexpr int kLdTileBytes = kLdChunks * kLdSlotBytes;
 constexpr int kLdThreads = 192;
 constexpr float kLdLazy = 6.0f;
 
 template <int HT>
 struct LdSmem {
-  uint8_t q[kLdChunks][HT * 128];               // the MMA reads 128 rows from each: into what follows
-  uint8_t p[HT * 128];
-  uint8_t ring[kLdSlots][kLdSlotBytes];
+  static constexpr int kStages = HT == 64 ? 4 : 5;
+  uint8_t q[kLdChunks][HT * 128];               // the MMA reads 64 rows from each: into what follows
+  uint8_t p[HT * 128];                          // P of two tiles side by side
+  uint8_t ring[kStages][kLdTileBytes];
   float fac[HT];
-  uint64_t full[kLdSlots], empty[kLdSlots];
-  uint64_t q_full, s_full[2], p_ready, pv_done, drain;
+  uint64_t full[kStages][kLdGroups], empty[kStages][kLdGroups];
+  uint64_t q_full, s_full[2], p_ready[2], pv_done[2], drain;
   uint32_t tmem;
   int abort;
   int b0, tile0, ntiles;                        // this CTA's range
@@ -108,21 +110,9 @@ __device__ __forceinline__ uint16_t ld_round(float x) {
 template <int DT>
 constexpr float kLdShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
 
-template <int CW>
-__device__ __forceinline__ void ld_columns(uint32_t taddr, uint32_t (&r)[CW]) {
-  if constexpr (CW == 32) {
-    tmem_ld_32x32b_x32(taddr, r);
-    tmem_wait_ld_regs(r);
-  } else {
-    tmem_ld_32x32b_x16(taddr, r);
-    tmem_wait_ld_regs16(r);
-  }
-}
-
 template <int DT, int HT>
 __global__ void __launch_bounds__(kLdThreads, 1)
     latent_decode_kernel(const __grid_constant__ CUtensorMap map_latent, const LdParams p) {
-  constexpr int CW = HT < 32 ? HT : 32;         // TMEM columns read at a time
   extern __shared__ uint8_t smem_raw[];
   LdSmem<HT>& sm = *reinterpret_cast<LdSmem<HT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                   ~static_cast<uintptr_t>(1023));
@@ -130,16 +120,19 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   const int ht = blockIdx.x, cta = blockIdx.y;  // row tiles fastest: those of one range run together
   const int R = p.q_len * p.Hq;
 
+  constexpr int kStages = LdSmem<HT>::kStages;
   if (tid == 0) {
-    for (int i = 0; i < kLdSlots; ++i) {
-      mbar_init(&sm.full[i], 1);
-      mbar_init(&sm.empty[i], 1);
+#pragma unroll 1
+    for (int i = 0; i < kStages * kLdGroups; ++i) {
+      mbar_init(&sm.full[0][0] + i, 1);
+      mbar_init(&sm.empty[0][0] + i, 1);
     }
     mbar_init(&sm.q_full, 4);
-    mbar_init(&sm.s_full[0], 1);
-    mbar_init(&sm.s_full[1], 1);
-    mbar_init(&sm.p_ready, 4);
-    mbar_init(&sm.pv_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.pv_done[i], 1);
+    }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -181,265 +174,293 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem, tO = tmem + 128;
+  const uint32_t tmem = sm.tmem, tO = tmem + 2 * kLdKeys;
   const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
   const int total = sm.ntiles;
 
   if (warp == 4) {
-    if (lane == 0 && total > 0) {
-      const int n_box = kLdKeys / p.box_rows;
-      // First latent row of each box of request b's key tile t (-1: at or behind the request's end).
-      auto box_rows = [&](int b, int t, int n, int (&rows)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int s = t * kLdKeys + i * p.box_rows;
-          rows[i] = -1;
-          if (i < n_box && s < n) {
-            int blk = __ldg(&p.block_table[static_cast<int64_t>(b) * p.max_blocks + s / p.block_size]);
-            if (blk < 0 || blk >= p.n_blocks) {
-              record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_BLOCK_TABLE);
-              blk = 0;
-            }
-            rows[i] = blk * p.block_size + s % p.block_size;
-          }
+    if (total > 0) {
+      // Lane i holds box i of a tile: its first latent row, -1 at or behind the request's end.
+      const bool has_box = lane * p.box_rows < kLdKeys;
+      auto box_row = [&](int b, int t, int n) {
+        const int s = t * kLdKeys + lane * p.box_rows;
+        if (!has_box || s >= n) return -1;
+        int blk = __ldg(&p.block_table[static_cast<int64_t>(b) * p.max_blocks + s / p.block_size]);
+        if (blk < 0 || blk >= p.n_blocks) {
+          record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_BLOCK_TABLE);
+          blk = 0;
         }
+        return blk * p.block_size + s % p.block_size;
       };
-      int b = sm.b0, t = sm.tile0, left = total;
-      int n = ld_len(p, b), rows[8];
-      box_rows(b, t, n, rows);
-      uint32_t g = 0;                           // chunks issued
+      const int n_box = kLdKeys / p.box_rows;
+      int b = sm.b0, t = sm.tile0, n = ld_len(p, b), row = box_row(b, t, n), done = 0, st = 0, ph = 0;
       bool ok = true;
-      while (left > 0 && ok) {
-        int cur[8], bytes = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cur[i] = rows[i];
-          if (cur[i] >= 0) bytes += p.box_rows * 128;
-        }
-        if (--left > 0) {                       // the next tile's table entries, a tile ahead
+      for (; done < total && ok; ++done) {
+        const int cur = row;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, cur >= 0), bytes = __popc(valid) * p.box_rows * 128;
+        if (done + 1 < total) {                 // the next tile's table entries, a tile ahead
           if (++t >= (n + kLdKeys - 1) / kLdKeys) {
             t = 0;
+#pragma unroll 1
             do n = ld_len(p, ++b);
             while (n == 0);
           }
-          box_rows(b, t, n, rows);
+          row = box_row(b, t, n);
         }
-        for (int c = 0; c < kLdChunks; ++c, ++g) {
-          const uint32_t s = g % kLdSlots;
-          ok = mbar_wait(&sm.empty[s], ((g / kLdSlots) & 1u) ^ 1u, ctl, DETAIL_WAIT_KEMPTY);
+#pragma unroll 1
+        for (int g = 0, c = 0; g < kLdGroups; ++g) {
+          ok = mbar_wait_warp(&sm.empty[st][g], ph ^ 1, ctl, DETAIL_WAIT_KEMPTY);
           if (!ok) break;
-          mbar_arrive_expect_tx(&sm.full[s], bytes);
-          const int x = c == 0 ? kLdDv : (c - 1) * 64;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (cur[i] >= 0) tma_load_3d(sm.ring[s] + i * p.box_rows * 128, &map_latent, x, 0, cur[i], &sm.full[s]);
+          const int c1 = 2 * g + 3;
+          if (elect_one()) mbar_arrive_expect_tx(&sm.full[st][g], bytes * (c1 - c));
+#pragma unroll 1
+          for (; c < c1; ++c)
+#pragma unroll 1
+            for (int i = 0; i < n_box; ++i) {
+              const int first = __shfl_sync(0xFFFFFFFFu, cur, i);
+              // the latent's last chunk, which is only a key, comes first
+              if (first >= 0 && elect_one())
+                tma_load_3d(sm.ring[st] + c * kLdSlotBytes + i * p.box_rows * 128, &map_latent,
+                            c == 0 ? kLdDv : (c - 1) * 64, 0, first, &sm.full[st][g]);
+            }
         }
+        if (++st == kStages) st = 0, ph ^= 1;
       }
-      // Let every copy land before the CTA exits (bounded).
-      for (uint32_t s = 0; s < kLdSlots; ++s)
-        if (g > s) mbar_wait_drain(&sm.full[s], ((g - s - 1) / kLdSlots) & 1u, p.budget_ns);
+      // Let every copy land before the CTA exits (bounded). Where a wait failed, groups that were not
+      // loaded run into the bound.
+      if (lane == 0) {
+#pragma unroll 1
+        for (int i = max(0, done - kStages); i < done; ++i)
+#pragma unroll 1
+          for (int g = 0; g < kLdGroups; ++g) mbar_drain_call(&sm.full[i % kStages][g], (i / kStages) & 1, p.budget_ns);
+      }
     }
     __syncwarp();
   } else if (warp == 5) {
-    if (lane == 0 && total > 0) {
+    // One thread, picked by elect: the compiler then knows that the MMAs' operands are uniform (29 cycles
+    // an MMA; 54 where a lane number picks the thread).
+    if (total > 0 && elect_one()) {
       constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
-      constexpr uint32_t idesc_qk = make_idesc_16(bf16, 128, kLdKeys);
+      constexpr uint32_t idesc_qk = make_idesc_16(bf16, 64, kLdKeys);
       constexpr uint32_t idesc_pv = make_idesc_16(bf16, 128, HT) | kIdescAMnMajor;
-      // Tiles of the segment that QK and PV are in, and their tiles so far.
-      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, chunk = 0;
-      int vb = qb, v_left = q_left, pv = 0;
+      // QK and PV walk the segments on their own: tiles left in the segment each is in.
+      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, g = 0, q_st = 0, q_ph = 0;
+      int vb = qb, v_left = q_left, pv = 0, v_st = 0;
       bool v_first = true, q_seen = false;
+      uint32_t idle = 0;
       uint64_t since = 0;
-      bool ok = true;
+      const uint64_t dq0 = make_smem_desc(smem_u32(sm.q[0]), 128), dk0 = make_smem_desc(smem_u32(sm.ring[0]), 128);
+      const uint64_t dv0 = make_smem_desc_mn(smem_u32(sm.ring[0]) + kLdSlotBytes, kLdSlotBytes, 1024);
+      const uint64_t dp0 = make_smem_desc(smem_u32(sm.p), 128);
       while (pv < total) {
-        bool moved = false;
-        if (pv < qk && mbar_try_wait(&sm.p_ready, pv & 1)) {
+        if (pv < qk && mbar_test(&sm.p_ready[pv & 1], (pv >> 1) & 1)) {
+          // A P that is there goes first: its tile's slots are what the loads wait for.
           tc_fence_after();
-          const uint32_t s0 = (pv & 1) * kLdChunks + 1;  // first value slot of the tile
-          const uint64_t db = make_smem_desc(smem_u32(sm.p), 128);
+          const uint64_t dv = dv0 + v_st * (kLdTileBytes >> 4), dp = dp0 + (pv & 1) * (kLdKeys * 2 >> 4);
 #pragma unroll
           for (int mt = 0; mt < 4; ++mt) {
-            const uint32_t va = smem_u32(sm.ring[s0 + 2 * mt]);
 #pragma unroll
             for (int kk = 0; kk < kLdKeys / 16; ++kk)
-              tc_mma_bf16(tO + mt * HT, make_smem_desc_mn(va + kk * 2048, kLdSlotBytes, 1024), db + 2ull * kk, idesc_pv,
+              tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc_pv,
                           (!v_first || kk > 0) ? 1u : 0u);
-            tc_commit(&sm.empty[s0 + 2 * mt]);
-            tc_commit(&sm.empty[s0 + 2 * mt + 1]);
+            tc_commit(&sm.empty[v_st][mt]);
           }
-          tc_commit(&sm.pv_done);
+          tc_commit(&sm.pv_done[pv & 1]);
           ++pv;
+          if (++v_st == kStages) v_st = 0;
           v_first = false;
           if (--v_left == 0 && pv < total) {
+#pragma unroll 1
             do v_left = min(ld_tiles(p, ++vb), total - pv);
             while (v_left == 0);
             v_first = true;
           }
-          moved = true;
-        } else if (qk < total && qk < pv + 2) {
-          // S[qk & 1] is free: the P of tile qk - 2 has been seen
-          if (!q_seen) q_seen = mbar_try_wait(&sm.q_full, q_seg & 1);
-          const uint32_t slot = (qk & 1) * kLdChunks + chunk;
-          if (q_seen && mbar_try_wait(&sm.full[slot], (qk >> 1) & 1)) {
+          idle = 0, since = 0;
+          continue;
+        }
+        if (qk < total && qk < pv + 2) {        // S[qk & 1] is free: the P of tile qk - 2 has been seen
+          if (!q_seen) q_seen = mbar_test(&sm.q_full, q_seg & 1);
+          if (q_seen && mbar_test(&sm.full[q_st][g], q_ph)) {
             tc_fence_after();
-            const uint64_t da = make_smem_desc(smem_u32(sm.q[chunk]), 128);
-            const uint64_t db = make_smem_desc(smem_u32(sm.ring[slot]), 128);
+            const int c0 = g == 0 ? 0 : 2 * g + 1, c1 = 2 * g + 3;
+            uint64_t dq = dq0 + c0 * (HT * 128 >> 4), dk = dk0 + q_st * (kLdTileBytes >> 4) + c0 * (kLdSlotBytes >> 4);
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c, dq += HT * 128 >> 4, dk += kLdSlotBytes >> 4)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(tmem + (qk & 1) * kLdKeys, da + 2ull * kk, db + 2ull * kk, idesc_qk,
-                          (chunk > 0 || kk > 0) ? 1u : 0u);
-            if (chunk == 0) tc_commit(&sm.empty[slot]);
-            if (++chunk == kLdChunks) {
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_bf16(tmem + (qk & 1) * kLdKeys, dq + 2ull * kk, dk + 2ull * kk, idesc_qk,
+                            (c > 0 || kk > 0) ? 1u : 0u);
+            if (++g == kLdGroups) {
               tc_commit(&sm.s_full[qk & 1]);
-              chunk = 0;
+              g = 0;
               ++qk;
+              if (++q_st == kStages) q_st = 0, q_ph ^= 1;
               if (--q_left == 0 && qk < total) {
+#pragma unroll 1
                 do q_left = min(ld_tiles(p, ++qb), total - qk);
                 while (q_left == 0);
                 ++q_seg;
                 q_seen = false;
               }
             }
-            moved = true;
+            idle = 0, since = 0;
+            continue;
           }
         }
-        if (moved) {
-          since = 0;
-        } else {
+        if ((++idle & 63u) == 0) {              // the timer's read is slow against a poll
+          if (*ctl.abort) break;
           const uint64_t now = globaltimer_ns();
           if (since == 0) since = now;
-          if (*ctl.abort) ok = false;
-          else if (now - since > p.budget_ns) {
+          if (now - since > p.budget_ns) {
             *ctl.abort = 1;
             record_error(p.hdr, DSA_ERR_TIMEOUT, DETAIL_WAIT_KFULL);
-            ok = false;
+            break;
           }
-          if (!ok) break;
         }
       }
       tc_commit(&sm.drain);
-      mbar_wait_drain(&sm.drain, 0, p.budget_ns);
+      mbar_drain_call(&sm.drain, 0, p.budget_ns);
     }
     __syncwarp();
   } else {
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    const int row = warp * 32 + lane, r = ht * HT + row;  // row of the tile, of the request
-    const bool softmax_warp = warp * 32 < HT;
-    int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0;
+    // S of a 64-row MMA has rows 16 w .. 16 w + 15 on the first 16 TMEM lanes of warp w's quarter.
+    const int row = warp * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
+    const bool softmax_warp = warp * 16 < HT, mine = softmax_warp && lane < 16;
+    int b = sm.b0, t = sm.tile0, left = total, done = 0;
     bool ok = true;
-    for (; left > 0; ++b, t = 0) {
+    // A request's queries into shared memory (zeros behind the last row), in flight on return.
+    auto load_q = [&](int b) {
+      const uint16_t* qb = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
+#pragma unroll 4
+      for (int u = tid; u < HT * kLdDqk / 8; u += 128) {
+        const int qr = u / (kLdDqk / 8), x = u % (kLdDqk / 8), rr = ht * HT + qr;
+        const int chunk = x >= kLdDv / 8 ? 0 : x / 8 + 1;
+        const uint16_t* src = rr < R ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h + x * 8 : qb;
+        cp_async_16(sm.q[chunk] + sw128(qr, x & 7), src, rr < R ? 16u : 0u);
+      }
+      cp_async_commit();
+    };
+    auto q_landed = [&]() {
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+    if (total > 0) {
+      load_q(b);
+      q_landed();
+    }
+    while (left > 0) {
       const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left);
-      if (te <= t) continue;
       left -= te - t;
-      // The segment's queries (zeros behind the last row); the QK products of the segment before are
-      // done: this warp has seen their last S.
-      {
-        const uint16_t* qb = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
-        for (int u = tid; u < HT * kLdDqk / 8; u += 128) {
-          const int qr = u / (kLdDqk / 8), x = u % (kLdDqk / 8), rr = ht * HT + qr;
-          const int chunk = x >= kLdDv / 8 ? 0 : x / 8 + 1;
-          const uint16_t* src = rr < R ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h + x * 8 : qb;
-          cp_async_16(sm.q[chunk] + sw128(qr, x & 7), src, rr < R ? 16u : 0u);
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_full);
-        ++seg;
+      int next = b;                             // the request of the segment after this one
+      if (left > 0) {
+#pragma unroll 1
+        do ++next;
+        while (ld_len(p, next) == 0);
       }
       const int sees = r < R ? max(0, n - p.q_len + 1 + r / p.Hq) : n;
       float m = -INFINITY, l = 0.0f;
       const int t_first = t;
+#pragma unroll 1
       for (; t < te; ++t, ++done) {
-        ok = mbar_wait(&sm.s_full[done & 1], (done >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
-        if (!named_bar_and(1, 128, ok)) { ok = false; break; }
-        tc_fence_after();
-        uint32_t s[2][32];
+        uint32_t s[32];
         float mn = m;
         bool grow = false;
         if (softmax_warp) {
-          const uint32_t tS = tmem + (done & 1) * kLdKeys + lanes;
-          tmem_ld_32x32b_x32(tS, s[0]);
-          tmem_ld_32x32b_x32(tS + 32, s[1]);
-          tmem_wait_ld_regs(s[0]);
-          tmem_wait_ld_regs(s[1]);
+          ok = mbar_wait_warp(&sm.s_full[done & 1], (done >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
+          tc_fence_after();
+          tmem_ld_32x32b_x32(tmem + (done & 1) * kLdKeys + lanes, s);
+          tmem_wait_ld_regs(s);
           const int seen = sees - t * kLdKeys;  // visible keys of this tile
           if (__any_sync(0xFFFFFFFFu, seen < kLdKeys)) {
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (e >= seen) s[e >> 5][e & 31] = 0xFF800000u;  // -inf
+            for (int e = 0; e < 32; ++e)
+              if (e >= seen) s[e] = 0xFF800000u;  // -inf
           }
           float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 64; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e >> 5][e & 31]));
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
           mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // (-inf - -inf is NaN and compares false)
-          grow = row < HT && t > t_first && (mn - m) * p.scale_log2 > kLdLazy;
+          grow = mine && t > t_first && (mn - m) * p.scale_log2 > kLdLazy;
+          if (t == t_first) m = mn;
         }
-        // P's buffer is free, and O^T may be rescaled, once the PV of the tile before is done.
-        if (t > t_first) ok = mbar_wait(&sm.pv_done, (done - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
-        if (t == t_first) m = mn;
-        if (named_bar_or(2, 128, grow)) {
-          if (softmax_warp) {
+        if (named_bar_or(1, 128, grow || !ok)) {
+          // Rare: some row's maximum has grown, or a wait has failed.
+          if (named_bar_or(2, 128, !ok)) {
+            ok = false;
+            break;
+          }
+          if (mine) {
             const float f = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * p.scale_log2);
             m = mn;
             l *= f;
-            if (row < HT) sm.fac[row] = f;
+            sm.fac[row] = f;
           }
           named_bar(3, 128);
+          ok = mbar_wait_warp(&sm.pv_done[(done - 1) & 1], ((done - 1) >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < 4 * HT; c += CW) {
-            uint32_t o[CW];
-            ld_columns<CW>(tO + lanes + c, o);
+          for (int c = 0; c < 4 * HT; c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tO + lanes + c, o);
+            tmem_wait_ld_regs16(o);
 #pragma unroll
-            for (int e = 0; e < CW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[(c & (HT - 1)) + e]);
-            if constexpr (CW == 32) tmem_st_32x32b_x32(tO + lanes + c, o);
-            else tmem_st_32x32b_x16(tO + lanes + c, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[(c & (HT - 1)) + e]);
+            tmem_st_32x32b_x16(tO + lanes + c, o);
           }
           tmem_wait_st();
         }
-        if (softmax_warp && row < HT) {
-          const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        // (The barrier above: S of this tile is complete, so the queries' buffer and, of the tile's rows
+        // behind the request's end, the shared memory may be written.)
+        if (t == te - 1 && left > 0) load_q(next);
+        if (softmax_warp) {
+          // P's half of the buffer is free once the PV of two tiles ago is done.
+          if (done >= 2)
+            ok = mbar_wait_warp(&sm.pv_done[done & 1], ((done >> 1) & 1) ^ 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
+          if (mine) {
+            const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            uint32_t w4[4];
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w4[4];
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const int k = u * 8 + e;
-              const float p0 = exp2_fast(fmaf(__uint_as_float(s[k >> 5][k & 31]), p.scale_log2, base));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(s[(k + 1) >> 5][(k + 1) & 31]), p.scale_log2, base));
-              sum[e & 2] += p0;
-              sum[(e & 2) + 1] += p1;
-              w4[e >> 1] = ld_pack<DT>(p0, p1);
+              for (int e = 0; e < 8; e += 2) {
+                const float p0 = exp2_fast(fmaf(__uint_as_float(s[u * 8 + e]), p.scale_log2, base));
+                const float p1 = exp2_fast(fmaf(__uint_as_float(s[u * 8 + e + 1]), p.scale_log2, base));
+                sum[e & 2] += p0;
+                sum[(e & 2) + 1] += p1;
+                w4[e >> 1] = ld_pack<DT>(p0, p1);
+              }
+              *reinterpret_cast<uint4*>(sm.p + sw128(row, (done & 1) * 4 + u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
-            *reinterpret_cast<uint4*>(sm.p + sw128(row, u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
         if ((t + 1) * kLdKeys > n) {
           // Rows behind the request's last key hold anything: zero weights must meet zeros.
-          const int key = tid >> 1;
+          const int key = tid >> 2;
           if (key >= n - t * kLdKeys)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(sm.ring[(done & 1) * kLdChunks + 1 + 4 * (tid & 1) + c] + key * 128 + u * 16) =
-                    make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (1 + 2 * (tid & 3) + c) * kLdSlotBytes + key * 128 +
+                                          u * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready);
+        if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
       }
       if (!ok) break;
+      if (left > 0) q_landed();
       // The segment's result.
-      ok = mbar_wait(&sm.pv_done, (done - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+      ok = mbar_wait_warp(&sm.pv_done[(done - 1) & 1], ((done - 1) >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
       const bool whole = t_first == 0 && te == nt;
-      if (softmax_warp && row < HT) {
+      if (mine) {
         if (whole) {
           sm.fac[row] = l > 0.0f ? 1.0f / l : 0.0f;
           if (p.lse && r < R)
@@ -451,30 +472,36 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           ml[HT + row] = l;
         }
       }
-      if (!named_bar_and(1, 128, ok)) { ok = false; break; }
+      if (!named_bar_and(1, 128, ok)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       float* part = p.part + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * kLdDv * HT;
 #pragma unroll 1
-      for (int c = 0; c < 4 * HT; c += CW) {
-        uint32_t o[CW];
-        ld_columns<CW>(tO + lanes + c, o);
-        const int dim = c / HT * 128 + row, h0 = c & (HT - 1);
+      for (int c = 0; c < 4 * HT; c += 16) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(tO + lanes + c, o);
+        tmem_wait_ld_regs16(o);
+        const int dim = c / HT * 128 + warp * 32 + lane, h0 = c & (HT - 1);
         if (whole) {
+          uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT + h0) * kLdDv + dim;
 #pragma unroll
-          for (int e = 0; e < CW; ++e) {
-            const int rr = ht * HT + h0 + e;
-            if (rr < R)
-              p.out[(static_cast<int64_t>(b) * R + rr) * kLdDv + dim] =
-                  sm.fac[h0 + e] > 0.0f ? ld_round<DT>(__uint_as_float(o[e]) * sm.fac[h0 + e]) : static_cast<uint16_t>(0);
+          for (int e = 0; e < 16; ++e) {
+            const float f = sm.fac[h0 + e];
+            if (ht * HT + h0 + e < R)
+              out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[e]) * f) : static_cast<uint16_t>(0);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < CW; e += 4)
+          for (int e = 0; e < 16; e += 4)
             *reinterpret_cast<uint4*>(part + dim * HT + h0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();
       named_bar(1, 128);  // fac is read by all before the next segment writes it
+      b = next;
+      t = 0;
     }
   }
   __syncthreads();

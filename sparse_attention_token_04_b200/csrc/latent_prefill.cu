@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
 
   if (warp == 8) {
-    if (lane == 0) {
+    if (elect_one()) {
       auto load_q = [&](int w) {
         mbar_arrive_expect_tx(&sm.q_full[w], 3 * kLpBlock);
         for (int c = 0; c < 3; ++c)
@@ -131,14 +131,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       };
       auto load_k = [&](int j) {
         const int st = j % kLpKStages;
-        if (!mbar_wait(&sm.k_empty[st], ((j / kLpKStages) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
+        if (!mbar_wait_call(&sm.k_empty[st], ((j / kLpKStages) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
         mbar_arrive_expect_tx(&sm.k_full[st], 3 * kLpBlock);
         for (int c = 0; c < 2; ++c) tma_load_3d(sm.k[st][c], &map_k, c * 64, h, k0 + j * kLpTile, &sm.k_full[st]);
         tma_load_3d(sm.k[st][2], &map_pe, 0, 0, k0 + j * kLpTile, &sm.k_full[st]);
         return true;
       };
       auto load_v = [&](int j) {
-        if (!mbar_wait(&sm.v_empty, (j & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
+        if (!mbar_wait_call(&sm.v_empty, (j & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
         mbar_arrive_expect_tx(&sm.v_full, 2 * kLpBlock);
         for (int c = 0; c < 2; ++c) tma_load_3d(sm.v[c], &map_v, c * 64, h, k0 + j * kLpTile, &sm.v_full);
         return true;
@@ -159,17 +159,17 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         // Let every copy land before the CTA exits (bounded).
         for (int w = 0; w < 2; ++w)
-          if (nt[w] > 0) mbar_wait_drain(&sm.q_full[w], 0, p.budget_ns);
+          if (nt[w] > 0) mbar_drain_call(&sm.q_full[w], 0, p.budget_ns);
         for (int st = 0; st < kLpKStages; ++st) {
           const int n = (nk_issued - st + kLpKStages - 1) / kLpKStages;
-          if (n > 0) mbar_wait_drain(&sm.k_full[st], (n - 1) & 1, p.budget_ns);
+          if (n > 0) mbar_drain_call(&sm.k_full[st], (n - 1) & 1, p.budget_ns);
         }
-        if (nv_issued > 0) mbar_wait_drain(&sm.v_full, (nv_issued - 1) & 1, p.budget_ns);
+        if (nv_issued > 0) mbar_drain_call(&sm.v_full, (nv_issued - 1) & 1, p.budget_ns);
       }
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && n_tiles > 0) {
+    if (n_tiles > 0 && elect_one()) {
       constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
       constexpr uint32_t idesc_qk = make_idesc_16(bf16, kLpTile, kLpTile);
       constexpr uint32_t idesc_pv = make_idesc_16(bf16, kLpTile, 128) | kIdescBMnMajor;
@@ -193,10 +193,10 @@ __global__ void __launch_bounds__(kLpThreads, 1)
                        idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
         tc_commit(&sm.o_done[w]);
       };
-      bool ok = mbar_wait(&sm.k_full[0], 0, ctl, DETAIL_WAIT_KFULL);
+      bool ok = mbar_wait_call(&sm.k_full[0], 0, ctl, DETAIL_WAIT_KFULL);
       for (int w = 0; w < 2 && ok; ++w) {
         if (nt[w] == 0) continue;
-        ok = mbar_wait(&sm.q_full[w], 0, ctl, DETAIL_WAIT_QFULL);
+        ok = mbar_wait_call(&sm.q_full[w], 0, ctl, DETAIL_WAIT_QFULL);
         if (!ok) break;
         tc_fence_after();
         qk(w, 0);
@@ -206,15 +206,15 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         const int last = j < nt[1] ? 1 : 0;  // the query tile whose PV is the last of this key tile
         for (int w = 0; w < 2 && ok; ++w) {
           if (j < nt[w]) {
-            ok = mbar_wait(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL) &&
-                 mbar_wait(&sm.p_ready[w], j & 1, ctl, DETAIL_WAIT_SCORES);
+            ok = mbar_wait_call(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL) &&
+                 mbar_wait_call(&sm.p_ready[w], j & 1, ctl, DETAIL_WAIT_SCORES);
             if (!ok) break;
             tc_fence_after();
             pv(w, j);
             if (w == last) tc_commit(&sm.v_empty);
           }
           if (j + 1 < nt[w]) {
-            ok = mbar_wait(&sm.k_full[(j + 1) % kLpKStages], ((j + 1) / kLpKStages) & 1, ctl, DETAIL_WAIT_KFULL);
+            ok = mbar_wait_call(&sm.k_full[(j + 1) % kLpKStages], ((j + 1) / kLpKStages) & 1, ctl, DETAIL_WAIT_KFULL);
             if (!ok) break;
             tc_fence_after();
             qk(w, j + 1);
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         if (ok && j + 1 < n_tiles) tc_commit(&sm.k_empty[(j + 1) % kLpKStages]);
       }
       tc_commit(&sm.drain);
-      mbar_wait_drain(&sm.drain, 0, p.budget_ns);
+      mbar_drain_call(&sm.drain, 0, p.budget_ns);
     }
     __syncwarp();
   } else {
@@ -238,8 +238,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < nt[w]; ++j) {
-      ok = mbar_wait(&sm.s_full[w], j & 1, ctl, DETAIL_WAIT_ACCFULL);
-      if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+      ok = mbar_wait_warp(&sm.s_full[w], j & 1, ctl, DETAIL_WAIT_ACCFULL);
+      if (!ok) break;
       tc_fence_after();
       uint32_t s[4][32];
 #pragma unroll
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         m = mn;
       } else if (__any_sync(0xFFFFFFFFu, (mn - m) * p.scale_log2 > kLpLazy)) {
         // (-inf - -inf is NaN and compares false; the row's O is 0 then and stays so)
-        ok = mbar_wait(&sm.o_done[w], (j - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
-        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        ok = mbar_wait_warp(&sm.o_done[w], (j - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+        if (!ok) break;
         tc_fence_after();
         const float f = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * p.scale_log2);
         m = mn;
@@ -299,22 +299,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if ((j + 1) * kLpTile > nk) {
         // Rows of V behind the request's last key belong to others: zero weights must meet zeros.
-        ok = mbar_wait(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL);
+        ok = mbar_wait_warp(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL);
         if (ok && row >= nk - j * kLpTile)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sm.v[c] + row * 128 + u * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
-        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        if (!ok) break;
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.p_ready[w]);
     }
-    if (ok && nt[w] > 0) ok = mbar_wait(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
-    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
     tc_fence_after();
     if (ok && first < nq) {
       const float inv = l > 0.0f ? 1.0f / l : 0.0f;
