@@ -2,25 +2,24 @@
 // against all of the request's paged 576-wide latents, whose first 512 entries are the values.
 //
 // A request's query rows are its q_len * Hq (token, head) pairs, taken HT (16, 32 or 64) at a time.
-// For one row tile the requests' key tiles (64 keys each), laid end to end, are split into equal
+// For one row tile the requests' key tiles (32 keys each), laid end to end, are split into equal
 // contiguous ranges, one per CTA, so that every CTA streams the same number of tiles whatever the
 // lengths; the part of a range inside one request is a segment. A segment that is a whole request
 // writes its outputs, any other its unnormalised sums with m and l, and latent_combine_kernel joins
 // those of a request. The grid is one CTA per SM over all row tiles, so row tiles of the same
 // request run side by side and the second one finds the latents in L2.
 //
-// Per key tile: S = Q K^T (rows x 64 keys x 576) into TMEM, softmax numerators P to shared memory,
-// and O^T += V^T P^T (4 x 128 dims x rows x 64 keys). The latent tile in shared memory serves both
+// Per key tile: S = Q K^T (rows x 32 keys x 576) into TMEM, softmax numerators P to shared memory,
+// and O^T += V^T P^T (4 x 128 dims x rows x 32 keys). The latent tile in shared memory serves both
 // products: as K (dims contiguous, K-major) and as V^T (the same bytes, M-major), so every latent is
 // fetched once. O^T has the dims on TMEM lanes and the rows on columns: 4 * HT columns, which is what
 // leaves room beside it (512 dims of 64 rows in 32 bits are half of TMEM).
 //   warps 0-3  the queries of each segment into shared memory; softmax (thread = row, warps 0 and 1
 //              at most); O^T rescaled (thread = dim) only when some row's maximum has grown by more
 //              than 2^kLdLazy; the segment's outputs;
-//   warp 4     TMA: nine 64-dim chunks of 8 KB a tile, the last chunk of the latent first (it is only
-//              a key and is released first), into a ring of 18 (two tiles);
-//   warp 5     one thread issues the MMAs: a tile's PV as soon as its P is there, else the next QK
-//              chunk that has landed.
+//   warp 4     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
+//   warp 5     one thread issues the MMAs: a tile's PV once its P is there, else the next tile's QK, up
+//              to two QK ahead.
 // Bound by HBM for up to 64 rows a request (1152 B a key); with 128 rows the products (278528 FLOP a
 // key) take as long as the bytes.
 #include <algorithm>
@@ -37,7 +36,7 @@ namespace dsa {
 constexpr int kLdDqk = 576, kLdDv = 512;
 constexpr int kLdKeys = 32;                     // keys of a tile
 constexpr int kLdChunks = kLdDqk / 64;          // 9
-constexpr int kLdGroups = 4;                    // barriers of a tile: chunks 0-2, 3-4, 5-6, 7-8
+constexpr int kLdScores = 3;                    // S buffers: two QK products ahead of the PV
 constexpr int kLdSlotBytes = kLdKeys * 128;     // 4 KB: one chunk
 constexpr int kLdTileBytes = kLdChunks * kLdSlotBytes;
 constexpr int kLdThreads = 192;
@@ -50,8 +49,8 @@ struct LdSmem {
   uint8_t p[HT * 128];                          // P of two tiles side by side
   uint8_t ring[kStages][kLdTileBytes];
   float fac[HT];
-  uint64_t full[kStages][kLdGroups], empty[kStages][kLdGroups];
-  uint64_t q_full, s_full[2], p_ready[2], pv_done[2], drain;
+  uint64_t full[kStages], empty[kStages];       // empty: the tile's PV is done
+  uint64_t q_full, s_full[kLdScores], p_ready[2], drain;
   uint32_t tmem;
   int abort;
   int b0, tile0, ntiles;                        // this CTA's range
@@ -123,16 +122,13 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   constexpr int kStages = LdSmem<HT>::kStages;
   if (tid == 0) {
 #pragma unroll 1
-    for (int i = 0; i < kStages * kLdGroups; ++i) {
-      mbar_init(&sm.full[0][0] + i, 1);
-      mbar_init(&sm.empty[0][0] + i, 1);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.empty[i], 1);
     }
     mbar_init(&sm.q_full, 4);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_ready[i], 4);
-      mbar_init(&sm.pv_done[i], 1);
-    }
+    for (int i = 0; i < kLdScores; ++i) mbar_init(&sm.s_full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_ready[i], 4);
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
     fence_mbar_init();
@@ -174,17 +170,20 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem, tO = tmem + 2 * kLdKeys;
+  const uint32_t tmem = sm.tmem, tO = tmem + kLdScores * kLdKeys;
   const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
   const int total = sm.ntiles;
 
+  // Each of the two issuing roles runs in one thread that elect picks: the compiler then knows that the
+  // operands of its instructions are uniform (an MMA takes 29 cycles to issue instead of 54, a box of a
+  // TMA load 32 instead of 70; measured alone).
   if (warp == 4) {
-    if (total > 0) {
-      // Lane i holds box i of a tile: its first latent row, -1 at or behind the request's end.
-      const bool has_box = lane * p.box_rows < kLdKeys;
-      auto box_row = [&](int b, int t, int n) {
-        const int s = t * kLdKeys + lane * p.box_rows;
-        if (!has_box || s >= n) return -1;
+    if (total > 0 && elect_one()) {
+      const int n_box = kLdKeys / p.box_rows;
+      // First latent row of box i of request b's key tile t, -1 at or behind the request's end.
+      auto box_row = [&](int b, int t, int n, int i) {
+        const int s = t * kLdKeys + i * p.box_rows;
+        if (s >= n) return -1;
         int blk = __ldg(&p.block_table[static_cast<int64_t>(b) * p.max_blocks + s / p.block_size]);
         if (blk < 0 || blk >= p.n_blocks) {
           record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_BLOCK_TABLE);
@@ -192,130 +191,116 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         }
         return blk * p.block_size + s % p.block_size;
       };
-      const int n_box = kLdKeys / p.box_rows;
-      int b = sm.b0, t = sm.tile0, n = ld_len(p, b), row = box_row(b, t, n), done = 0, st = 0, ph = 0;
+      int b = sm.b0, t = sm.tile0, n = ld_len(p, b), row = box_row(b, t, n, 0), done = 0, st = 0, ph = 0;
       bool ok = true;
       for (; done < total && ok; ++done) {
-        const int cur = row;
-        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, cur >= 0), bytes = __popc(valid) * p.box_rows * 128;
-        if (done + 1 < total) {                 // the next tile's table entries, a tile ahead
+        const int cb = b, ct = t, cn = n, cur = row;
+        if (done + 1 < total) {                 // the next tile's first table entry, a tile ahead
           if (++t >= (n + kLdKeys - 1) / kLdKeys) {
             t = 0;
 #pragma unroll 1
             do n = ld_len(p, ++b);
             while (n == 0);
           }
-          row = box_row(b, t, n);
+          row = box_row(b, t, n, 0);
         }
+        uint8_t* ring = sm.ring[st];
+        ok = mbar_wait_call(&sm.empty[st], ph ^ 1, ctl, DETAIL_WAIT_KEMPTY);
+        if (!ok) break;
+        if (n_box == 1) {
+          mbar_arrive_expect_tx(&sm.full[st], kLdTileBytes);
+#pragma unroll
+          for (int c = 0; c < kLdChunks; ++c)
+            tma_load_3d(ring + c * kLdSlotBytes, &map_latent, c * 64, 0, cur, &sm.full[st]);
+        } else {
+          const int boxes = min(n_box, (cn - ct * kLdKeys + p.box_rows - 1) / p.box_rows);
+          mbar_arrive_expect_tx(&sm.full[st], kLdChunks * boxes * p.box_rows * 128);
 #pragma unroll 1
-        for (int g = 0, c = 0; g < kLdGroups; ++g) {
-          ok = mbar_wait_warp(&sm.empty[st][g], ph ^ 1, ctl, DETAIL_WAIT_KEMPTY);
-          if (!ok) break;
-          const int c1 = 2 * g + 3;
-          if (elect_one()) mbar_arrive_expect_tx(&sm.full[st][g], bytes * (c1 - c));
+          for (int i = 0; i < boxes; ++i) {
+            const int first = i == 0 ? cur : box_row(cb, ct, cn, i);
 #pragma unroll 1
-          for (; c < c1; ++c)
-#pragma unroll 1
-            for (int i = 0; i < n_box; ++i) {
-              const int first = __shfl_sync(0xFFFFFFFFu, cur, i);
-              // the latent's last chunk, which is only a key, comes first
-              if (first >= 0 && elect_one())
-                tma_load_3d(sm.ring[st] + c * kLdSlotBytes + i * p.box_rows * 128, &map_latent,
-                            c == 0 ? kLdDv : (c - 1) * 64, 0, first, &sm.full[st][g]);
-            }
+            for (int c = 0; c < kLdChunks; ++c)
+              tma_load_3d(ring + c * kLdSlotBytes + i * p.box_rows * 128, &map_latent, c * 64, 0, first, &sm.full[st]);
+          }
         }
         if (++st == kStages) st = 0, ph ^= 1;
       }
-      // Let every copy land before the CTA exits (bounded). Where a wait failed, groups that were not
-      // loaded run into the bound.
-      if (lane == 0) {
+      // Let every copy land before the CTA exits (bounded).
 #pragma unroll 1
-        for (int i = max(0, done - kStages); i < done; ++i)
-#pragma unroll 1
-          for (int g = 0; g < kLdGroups; ++g) mbar_drain_call(&sm.full[i % kStages][g], (i / kStages) & 1, p.budget_ns);
-      }
+      for (int i = max(0, done - kStages); i < done; ++i)
+        mbar_drain_call(&sm.full[i % kStages], (i / kStages) & 1, p.budget_ns);
     }
     __syncwarp();
   } else if (warp == 5) {
-    // One thread, picked by elect: the compiler then knows that the MMAs' operands are uniform (29 cycles
-    // an MMA; 54 where a lane number picks the thread).
     if (total > 0 && elect_one()) {
       constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
       constexpr uint32_t idesc_qk = make_idesc_16(bf16, 64, kLdKeys);
       constexpr uint32_t idesc_pv = make_idesc_16(bf16, 128, HT) | kIdescAMnMajor;
       // QK and PV walk the segments on their own: tiles left in the segment each is in.
-      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, g = 0, q_st = 0, q_ph = 0;
-      int vb = qb, v_left = q_left, pv = 0, v_st = 0;
-      bool v_first = true, q_seen = false;
-      uint32_t idle = 0;
-      uint64_t since = 0;
+      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, q_st = 0, q_ph = 0;
+      int q_buf = 0, vb = qb, v_left = q_left, pv = 0, v_st = 0;
+      uint32_t v_acc = 0;
+      bool ok = true, q_new = false;          // q_new: QK stands at a segment's first tile
       const uint64_t dq0 = make_smem_desc(smem_u32(sm.q[0]), 128), dk0 = make_smem_desc(smem_u32(sm.ring[0]), 128);
-      const uint64_t dv0 = make_smem_desc_mn(smem_u32(sm.ring[0]) + kLdSlotBytes, kLdSlotBytes, 1024);
+      const uint64_t dv0 = make_smem_desc_mn(smem_u32(sm.ring[0]), kLdSlotBytes, 1024);
       const uint64_t dp0 = make_smem_desc(smem_u32(sm.p), 128);
-      while (pv < total) {
-        if (pv < qk && mbar_test(&sm.p_ready[pv & 1], (pv >> 1) & 1)) {
-          // A P that is there goes first: its tile's slots are what the loads wait for.
-          tc_fence_after();
-          const uint64_t dv = dv0 + v_st * (kLdTileBytes >> 4), dp = dp0 + (pv & 1) * (kLdKeys * 2 >> 4);
+      auto issue_pv = [&]() {
+        tc_fence_after();
+        const uint64_t dv = dv0 + v_st * (kLdTileBytes >> 4), dp = dp0 + (pv & 1) * (kLdKeys * 2 >> 4);
 #pragma unroll
-          for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-            for (int kk = 0; kk < kLdKeys / 16; ++kk)
-              tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc_pv,
-                          (!v_first || kk > 0) ? 1u : 0u);
-            tc_commit(&sm.empty[v_st][mt]);
-          }
-          tc_commit(&sm.pv_done[pv & 1]);
-          ++pv;
-          if (++v_st == kStages) v_st = 0;
-          v_first = false;
-          if (--v_left == 0 && pv < total) {
+          for (int kk = 0; kk < kLdKeys / 16; ++kk)
+            tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc_pv,
+                        kk > 0 ? 1u : v_acc);
+        tc_commit(&sm.empty[v_st]);
+        ++pv;
+        if (++v_st == kStages) v_st = 0;
+        v_acc = 1;
+        if (--v_left == 0 && pv < total) {
 #pragma unroll 1
-            do v_left = min(ld_tiles(p, ++vb), total - pv);
-            while (v_left == 0);
-            v_first = true;
-          }
-          idle = 0, since = 0;
+          do v_left = min(ld_tiles(p, ++vb), total - pv);
+          while (v_left == 0);
+          v_acc = 0;
+        }
+      };
+#pragma unroll 1
+      while (pv < total) {
+        // A P that is there goes first: its tile's shared memory is what the loads wait for. It is waited
+        // for where no S buffer is free (the P of tile qk - kLdScores has not been seen) or no tile is
+        // left. Before a segment's first QK, which waits for that segment's queries, every PV but the last
+        // is issued: the queries come once the softmax of the segment before has got through, and it
+        // needs those.
+        const bool must = qk == total || qk >= pv + (q_new ? 2 : kLdScores);
+        if (must) ok = mbar_wait_call(&sm.p_ready[pv & 1], (pv >> 1) & 1, ctl, DETAIL_WAIT_SCORES);
+        if (!ok) break;
+        if (must || (pv < qk && mbar_test(&sm.p_ready[pv & 1], (pv >> 1) & 1))) {
+          issue_pv();
           continue;
         }
-        if (qk < total && qk < pv + 2) {        // S[qk & 1] is free: the P of tile qk - 2 has been seen
-          if (!q_seen) q_seen = mbar_test(&sm.q_full, q_seg & 1);
-          if (q_seen && mbar_test(&sm.full[q_st][g], q_ph)) {
-            tc_fence_after();
-            const int c0 = g == 0 ? 0 : 2 * g + 1, c1 = 2 * g + 3;
-            uint64_t dq = dq0 + c0 * (HT * 128 >> 4), dk = dk0 + q_st * (kLdTileBytes >> 4) + c0 * (kLdSlotBytes >> 4);
-#pragma unroll 1
-            for (int c = c0; c < c1; ++c, dq += HT * 128 >> 4, dk += kLdSlotBytes >> 4)
+        ok = mbar_wait_call(&sm.q_full, q_seg & 1, ctl, DETAIL_WAIT_QFULL) &&
+             mbar_wait_call(&sm.full[q_st], q_ph, ctl, DETAIL_WAIT_KFULL);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t dk = dk0 + q_st * (kLdTileBytes >> 4);
+        const uint32_t tS = tmem + q_buf * kLdKeys;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_bf16(tmem + (qk & 1) * kLdKeys, dq + 2ull * kk, dk + 2ull * kk, idesc_qk,
-                            (c > 0 || kk > 0) ? 1u : 0u);
-            if (++g == kLdGroups) {
-              tc_commit(&sm.s_full[qk & 1]);
-              g = 0;
-              ++qk;
-              if (++q_st == kStages) q_st = 0, q_ph ^= 1;
-              if (--q_left == 0 && qk < total) {
+        for (int c = 0; c < kLdChunks; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16(tS, dq0 + (c * HT * 128 >> 4) + 2ull * kk, dk + (c * kLdSlotBytes >> 4) + 2ull * kk, idesc_qk,
+                        c > 0 || kk > 0 ? 1u : 0u);
+        tc_commit(&sm.s_full[q_buf]);
+        ++qk;
+        q_new = false;
+        if (++q_buf == kLdScores) q_buf = 0;
+        if (++q_st == kStages) q_st = 0, q_ph ^= 1;
+        if (--q_left == 0 && qk < total) {
 #pragma unroll 1
-                do q_left = min(ld_tiles(p, ++qb), total - qk);
-                while (q_left == 0);
-                ++q_seg;
-                q_seen = false;
-              }
-            }
-            idle = 0, since = 0;
-            continue;
-          }
-        }
-        if ((++idle & 63u) == 0) {              // the timer's read is slow against a poll
-          if (*ctl.abort) break;
-          const uint64_t now = globaltimer_ns();
-          if (since == 0) since = now;
-          if (now - since > p.budget_ns) {
-            *ctl.abort = 1;
-            record_error(p.hdr, DSA_ERR_TIMEOUT, DETAIL_WAIT_KFULL);
-            break;
-          }
+          do q_left = min(ld_tiles(p, ++qb), total - qk);
+          while (q_left == 0);
+          ++q_seg;
+          q_new = true;
         }
       }
       tc_commit(&sm.drain);
@@ -327,17 +312,26 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     // S of a 64-row MMA has rows 16 w .. 16 w + 15 on the first 16 TMEM lanes of warp w's quarter.
     const int row = warp * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
     const bool softmax_warp = warp * 16 < HT, mine = softmax_warp && lane < 16;
-    int b = sm.b0, t = sm.tile0, left = total, done = 0;
+    int b = sm.b0, t = sm.tile0, left = total, done = 0, s_buf = 0, s_ph = 0;
     bool ok = true;
+    // Waits for the PV of the CTA's tile i.
+    auto pv_done = [&](int i) {
+      return mbar_wait_warp(&sm.empty[i % kStages], (i / kStages) & 1, ctl, DETAIL_WAIT_ACCFULL);
+    };
     // A request's queries into shared memory (zeros behind the last row), in flight on return.
     auto load_q = [&](int b) {
       const uint16_t* qb = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
-#pragma unroll 4
-      for (int u = tid; u < HT * kLdDqk / 8; u += 128) {
-        const int qr = u / (kLdDqk / 8), x = u % (kLdDqk / 8), rr = ht * HT + qr;
-        const int chunk = x >= kLdDv / 8 ? 0 : x / 8 + 1;
-        const uint16_t* src = rr < R ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h + x * 8 : qb;
-        cp_async_16(sm.q[chunk] + sw128(qr, x & 7), src, rr < R ? 16u : 0u);
+#pragma unroll 1
+      for (int qr = warp; qr < HT; qr += 4) {   // a warp takes a row: 72 units of 16 bytes
+        const int rr = ht * HT + qr;
+        const bool real = rr < R;
+        const uint16_t* src = real ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h : qb;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int x = lane + 32 * k;
+          if (x < kLdDqk / 8)
+            cp_async_16(sm.q[x / 8] + sw128(qr, x & 7), src + (real ? x * 8 : 0), real ? 16u : 0u);
+        }
       }
       cp_async_commit();
     };
@@ -369,9 +363,9 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         float mn = m;
         bool grow = false;
         if (softmax_warp) {
-          ok = mbar_wait_warp(&sm.s_full[done & 1], (done >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
+          ok = mbar_wait_warp(&sm.s_full[s_buf], s_ph, ctl, DETAIL_WAIT_ACCFULL) && ok;
           tc_fence_after();
-          tmem_ld_32x32b_x32(tmem + (done & 1) * kLdKeys + lanes, s);
+          tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s);
           tmem_wait_ld_regs(s);
           const int seen = sees - t * kLdKeys;  // visible keys of this tile
           if (__any_sync(0xFFFFFFFFu, seen < kLdKeys)) {
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             sm.fac[row] = f;
           }
           named_bar(3, 128);
-          ok = mbar_wait_warp(&sm.pv_done[(done - 1) & 1], ((done - 1) >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
+          ok = pv_done(done - 1);
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4 * HT; c += 16) {
@@ -418,8 +412,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         if (t == te - 1 && left > 0) load_q(next);
         if (softmax_warp) {
           // P's half of the buffer is free once the PV of two tiles ago is done.
-          if (done >= 2)
-            ok = mbar_wait_warp(&sm.pv_done[done & 1], ((done >> 1) & 1) ^ 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
+          if (done >= 2) ok = pv_done(done - 2) && ok;
           if (mine) {
             const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -447,18 +440,19 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (1 + 2 * (tid & 3) + c) * kLdSlotBytes + key * 128 +
+                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (2 * (tid & 3) + c) * kLdSlotBytes + key * 128 +
                                           u * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
+        if (++s_buf == kLdScores) s_buf = 0, s_ph ^= 1;
       }
       if (!ok) break;
       if (left > 0) q_landed();
       // The segment's result.
-      ok = mbar_wait_warp(&sm.pv_done[(done - 1) & 1], ((done - 1) >> 1) & 1, ctl, DETAIL_WAIT_ACCFULL) && ok;
+      ok = pv_done(done - 1) && ok;
       const bool whole = t_first == 0 && te == nt;
       if (mine) {
         if (whole) {
