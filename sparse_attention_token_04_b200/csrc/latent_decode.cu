@@ -18,8 +18,9 @@
 //              at most); O^T rescaled (thread = dim) only when some row's maximum has grown by more
 //              than 2^kLdLazy; the segment's outputs;
 //   warp 4     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
-//   warp 5     one thread issues the MMAs: a tile's PV once its P is there, else the next tile's QK, up
-//              to two QK ahead.
+//   warp 9     one thread issues the QK products, up to three tiles ahead of the softmax;
+//   warp 10    one thread issues the PV products. (With both in one thread the tensor core idled while
+//              that thread looked at its barriers.)
 // Bound by HBM for up to 64 rows a request (1152 B a key); with 128 rows the products (278528 FLOP a
 // key) take as long as the bytes.
 #include <algorithm>
@@ -39,7 +40,8 @@ constexpr int kLdChunks = kLdDqk / 64;          // 9
 constexpr int kLdScores = 3;                    // S buffers: two QK products ahead of the PV
 constexpr int kLdSlotBytes = kLdKeys * 128;     // 4 KB: one chunk
 constexpr int kLdTileBytes = kLdChunks * kLdSlotBytes;
-constexpr int kLdThreads = 192;
+constexpr int kLdThreads = 352;
+constexpr int kLdLead = 4;                      // rescale factors of this many tiles are kept
 constexpr float kLdLazy = 6.0f;
 
 template <int HT>
@@ -48,9 +50,10 @@ struct LdSmem {
   uint8_t q[kLdChunks][HT * 128];               // the MMA reads 64 rows from each: into what follows
   uint8_t p[HT * 128];                          // P of two tiles side by side
   uint8_t ring[kStages][kLdTileBytes];
-  float fac[HT];
+  float fac[kLdLead][HT], inv[HT];
+  int grow[kLdLead][4];                         // whether a softmax warp's factors are to be applied
   uint64_t full[kStages], empty[kStages];       // empty: the tile's PV is done
-  uint64_t q_full, s_full[kLdScores], p_ready[2], drain;
+  uint64_t q_full, s_full[kLdScores], m_ready[kLdLead], p_ready[2], seg_ready, seg_done, drain[2];
   uint32_t tmem;
   int abort;
   int b0, tile0, ntiles;                        // this CTA's range
@@ -66,7 +69,7 @@ struct LdParams {
   float scale, scale_log2;
   uint16_t* out;
   float* lse;
-  float* part;                                  // [row tiles][CTAs][2][512][HT] unnormalised O^T
+  float* part;                                  // [row tiles][CTAs][2][HT / 4][512][4] unnormalised O^T
   float* ml;                                    // [row tiles][CTAs][2][2][HT] m, l
   WsHeader* hdr;
   uint64_t budget_ns;
@@ -119,7 +122,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   const int ht = blockIdx.x, cta = blockIdx.y;  // row tiles fastest: those of one range run together
   const int R = p.q_len * p.Hq;
 
-  constexpr int kStages = LdSmem<HT>::kStages;
+  constexpr int kStages = LdSmem<HT>::kStages, kSoft = HT / 16;
   if (tid == 0) {
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) {
@@ -128,8 +131,12 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     }
     mbar_init(&sm.q_full, 4);
     for (int i = 0; i < kLdScores; ++i) mbar_init(&sm.s_full[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_ready[i], 4);
-    mbar_init(&sm.drain, 1);
+    for (int i = 0; i < kLdLead; ++i) mbar_init(&sm.m_ready[i], kSoft);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_ready[i], kSoft + 4);
+    mbar_init(&sm.seg_ready, kSoft);
+    mbar_init(&sm.seg_done, 4);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     }
     if (lane == 0) sm.ntiles = static_cast<int>(hi - lo);
   }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -173,11 +180,15 @@ __global__ void __launch_bounds__(kLdThreads, 1)
   const uint32_t tmem = sm.tmem, tO = tmem + kLdScores * kLdKeys;
   const WaitCtl ctl{p.hdr, &sm.abort, p.budget_ns};
   const int total = sm.ntiles;
+  // Waits (as a warp) for the PV of the CTA's tile i.
+  auto pv_done = [&](int i) {
+    return mbar_wait_warp(&sm.empty[i % kStages], (i / kStages) & 1, ctl, DETAIL_WAIT_ACCFULL);
+  };
 
   // Each of the two issuing roles runs in one thread that elect picks: the compiler then knows that the
   // operands of its instructions are uniform (an MMA takes 29 cycles to issue instead of 54, a box of a
   // TMA load 32 instead of 70; measured alone).
-  if (warp == 4) {
+  if (warp == 8) {
     if (total > 0 && elect_one()) {
       const int n_box = kLdKeys / p.box_rows;
       // First latent row of box i of request b's key tile t, -1 at or behind the request's end.
@@ -231,142 +242,106 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         mbar_drain_call(&sm.full[i % kStages], (i / kStages) & 1, p.budget_ns);
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     if (total > 0 && elect_one()) {
-      constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
-      constexpr uint32_t idesc_qk = make_idesc_16(bf16, 64, kLdKeys);
-      constexpr uint32_t idesc_pv = make_idesc_16(bf16, 128, HT) | kIdescAMnMajor;
-      // QK and PV walk the segments on their own: tiles left in the segment each is in.
-      int qb = sm.b0, q_left = min(ld_tiles(p, qb) - sm.tile0, total), q_seg = 0, qk = 0, q_st = 0, q_ph = 0;
-      int q_buf = 0, vb = qb, v_left = q_left, pv = 0, v_st = 0;
-      uint32_t v_acc = 0;
-      bool ok = true, q_new = false;          // q_new: QK stands at a segment's first tile
-      const uint64_t dq0 = make_smem_desc(smem_u32(sm.q[0]), 128), dk0 = make_smem_desc(smem_u32(sm.ring[0]), 128);
-      const uint64_t dv0 = make_smem_desc_mn(smem_u32(sm.ring[0]), kLdSlotBytes, 1024);
-      const uint64_t dp0 = make_smem_desc(smem_u32(sm.p), 128);
-      auto issue_pv = [&]() {
-        tc_fence_after();
-        const uint64_t dv = dv0 + v_st * (kLdTileBytes >> 4), dp = dp0 + (pv & 1) * (kLdKeys * 2 >> 4);
-#pragma unroll
-        for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-          for (int kk = 0; kk < kLdKeys / 16; ++kk)
-            tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc_pv,
-                        kk > 0 ? 1u : v_acc);
-        tc_commit(&sm.empty[v_st]);
-        ++pv;
-        if (++v_st == kStages) v_st = 0;
-        v_acc = 1;
-        if (--v_left == 0 && pv < total) {
+      constexpr uint32_t idesc = make_idesc_16(DT == DSA_DTYPE_BF16 ? 1u : 0u, 64, kLdKeys);
+      int b = sm.b0, left = min(ld_tiles(p, b) - sm.tile0, total), seg = 0, st = 0, ph = 0, buf = 0;
+      const uint64_t dq = make_smem_desc(smem_u32(sm.q[0]), 128), dk0 = make_smem_desc(smem_u32(sm.ring[0]), 128);
+      bool ok = mbar_wait_call(&sm.q_full, 0, ctl, DETAIL_WAIT_QFULL);
 #pragma unroll 1
-          do v_left = min(ld_tiles(p, ++vb), total - pv);
-          while (v_left == 0);
-          v_acc = 0;
-        }
-      };
+      for (int t = 0; t < total && ok; ++t) {
+        if (left == 0) {                        // the next segment, once its queries are there
 #pragma unroll 1
-      while (pv < total) {
-        // A P that is there goes first: its tile's shared memory is what the loads wait for. It is waited
-        // for where no S buffer is free (the P of tile qk - kLdScores has not been seen) or no tile is
-        // left. Before a segment's first QK, which waits for that segment's queries, every PV but the last
-        // is issued: the queries come once the softmax of the segment before has got through, and it
-        // needs those.
-        const bool must = qk == total || qk >= pv + (q_new ? 2 : kLdScores);
-        if (must) ok = mbar_wait_call(&sm.p_ready[pv & 1], (pv >> 1) & 1, ctl, DETAIL_WAIT_SCORES);
-        if (!ok) break;
-        if (must || (pv < qk && mbar_test(&sm.p_ready[pv & 1], (pv >> 1) & 1))) {
-          issue_pv();
-          continue;
+          do left = min(ld_tiles(p, ++b), total - t);
+          while (left == 0);
+          ++seg;
+          ok = mbar_wait_call(&sm.q_full, seg & 1, ctl, DETAIL_WAIT_QFULL);
         }
-        ok = mbar_wait_call(&sm.q_full, q_seg & 1, ctl, DETAIL_WAIT_QFULL) &&
-             mbar_wait_call(&sm.full[q_st], q_ph, ctl, DETAIL_WAIT_KFULL);
+        // An S buffer is free once the scores of the tile that had it have been read.
+        const int u = t - kLdScores;
+        if (ok && u >= 0) ok = mbar_wait_call(&sm.m_ready[u % kLdLead], (u / kLdLead) & 1, ctl, DETAIL_WAIT_SCORES);
+        ok = ok && mbar_wait_call(&sm.full[st], ph, ctl, DETAIL_WAIT_KFULL);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t dk = dk0 + q_st * (kLdTileBytes >> 4);
-        const uint32_t tS = tmem + q_buf * kLdKeys;
+        const uint64_t dk = dk0 + st * (kLdTileBytes >> 4);
 #pragma unroll
         for (int c = 0; c < kLdChunks; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(tS, dq0 + (c * HT * 128 >> 4) + 2ull * kk, dk + (c * kLdSlotBytes >> 4) + 2ull * kk, idesc_qk,
-                        c > 0 || kk > 0 ? 1u : 0u);
-        tc_commit(&sm.s_full[q_buf]);
-        ++qk;
-        q_new = false;
-        if (++q_buf == kLdScores) q_buf = 0;
-        if (++q_st == kStages) q_st = 0, q_ph ^= 1;
-        if (--q_left == 0 && qk < total) {
-#pragma unroll 1
-          do q_left = min(ld_tiles(p, ++qb), total - qk);
-          while (q_left == 0);
-          ++q_seg;
-          q_new = true;
-        }
+            tc_mma_bf16(tmem + buf * kLdKeys, dq + (c * HT * 128 >> 4) + 2ull * kk,
+                        dk + (c * kLdSlotBytes >> 4) + 2ull * kk, idesc, c > 0 || kk > 0 ? 1u : 0u);
+        tc_commit(&sm.s_full[buf]);
+        --left;
+        if (++buf == kLdScores) buf = 0;
+        if (++st == kStages) st = 0, ph ^= 1;
       }
-      tc_commit(&sm.drain);
-      mbar_drain_call(&sm.drain, 0, p.budget_ns);
+      tc_commit(&sm.drain[0]);
+      mbar_drain_call(&sm.drain[0], 0, p.budget_ns);
     }
     __syncwarp();
-  } else {
-    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-    // S of a 64-row MMA has rows 16 w .. 16 w + 15 on the first 16 TMEM lanes of warp w's quarter.
-    const int row = warp * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
-    const bool softmax_warp = warp * 16 < HT, mine = softmax_warp && lane < 16;
-    int b = sm.b0, t = sm.tile0, left = total, done = 0, s_buf = 0, s_ph = 0;
-    bool ok = true;
-    // Waits for the PV of the CTA's tile i.
-    auto pv_done = [&](int i) {
-      return mbar_wait_warp(&sm.empty[i % kStages], (i / kStages) & 1, ctl, DETAIL_WAIT_ACCFULL);
-    };
-    // A request's queries into shared memory (zeros behind the last row), in flight on return.
-    auto load_q = [&](int b) {
-      const uint16_t* qb = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
+  } else if (warp == 10) {
+    if (total > 0 && elect_one()) {
+      constexpr uint32_t idesc = make_idesc_16(DT == DSA_DTYPE_BF16 ? 1u : 0u, 128, HT) | kIdescAMnMajor;
+      int b = sm.b0, left = min(ld_tiles(p, b) - sm.tile0, total), st = 0;
+      uint32_t acc = 0;                         // 0: the segment's first tile
+      const uint64_t dv0 = make_smem_desc_mn(smem_u32(sm.ring[0]), kLdSlotBytes, 1024);
+      const uint64_t dp0 = make_smem_desc(smem_u32(sm.p), 128);
 #pragma unroll 1
-      for (int qr = warp; qr < HT; qr += 4) {   // a warp takes a row: 72 units of 16 bytes
-        const int rr = ht * HT + qr;
-        const bool real = rr < R;
-        const uint16_t* src = real ? qb + (rr / p.Hq) * p.qs_t + (rr % p.Hq) * p.qs_h : qb;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int x = lane + 32 * k;
-          if (x < kLdDqk / 8)
-            cp_async_16(sm.q[x / 8] + sw128(qr, x & 7), src + (real ? x * 8 : 0), real ? 16u : 0u);
+      for (int t = 0; t < total; ++t) {
+        if (left == 0) {
+#pragma unroll 1
+          do left = min(ld_tiles(p, ++b), total - t);
+          while (left == 0);
+          acc = 0;
         }
+        // (A tile whose P is there has landed: its scores came from it.)
+        if (!mbar_wait_call(&sm.p_ready[t & 1], (t >> 1) & 1, ctl, DETAIL_WAIT_SCORES)) break;
+        tc_fence_after();
+        const uint64_t dv = dv0 + st * (kLdTileBytes >> 4), dp = dp0 + (t & 1) * (kLdKeys * 2 >> 4);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int kk = 0; kk < kLdKeys / 16; ++kk)
+            tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc,
+                        kk > 0 ? 1u : acc);
+        tc_commit(&sm.empty[st]);
+        --left;
+        acc = 1;
+        if (++st == kStages) st = 0;
       }
-      cp_async_commit();
-    };
-    auto q_landed = [&]() {
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
-    };
-    if (total > 0) {
-      load_q(b);
-      q_landed();
+      tc_commit(&sm.drain[1]);
+      mbar_drain_call(&sm.drain[1], 0, p.budget_ns);
     }
-    while (left > 0) {
-      const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left);
-      left -= te - t;
-      int next = b;                             // the request of the segment after this one
-      if (left > 0) {
+    __syncwarp();
+  } else if (warp < 4) {
+    // Softmax. S of a 64-row MMA has rows 16 w .. 16 w + 15 on the first 16 TMEM lanes of warp w's
+    // quarter: the other half of the warp idles along.
+    if (warp < kSoft && total > 0) {
+      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+      const int row = warp * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
+      const bool mine = lane < 16;
+      int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0, s_buf = 0, s_ph = 0;
+      bool ok = true, have = false;             // have: s holds the tile's scores already
+      uint32_t s[32], s_next[32];
+      while (left > 0 && ok) {
+        const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left), t_first = t;
+        if (te <= t) {                          // a request without keys
+          ++b;
+          continue;
+        }
+        left -= te - t;
+        const int sees = r < R ? max(0, n - p.q_len + 1 + r / p.Hq) : n;
+        float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-        do ++next;
-        while (ld_len(p, next) == 0);
-      }
-      const int sees = r < R ? max(0, n - p.q_len + 1 + r / p.Hq) : n;
-      float m = -INFINITY, l = 0.0f;
-      const int t_first = t;
-#pragma unroll 1
-      for (; t < te; ++t, ++done) {
-        uint32_t s[32];
-        float mn = m;
-        bool grow = false;
-        if (softmax_warp) {
-          ok = mbar_wait_warp(&sm.s_full[s_buf], s_ph, ctl, DETAIL_WAIT_ACCFULL) && ok;
-          tc_fence_after();
-          tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s);
-          tmem_wait_ld_regs(s);
+        for (; t < te; ++t, ++done) {
+          if (!have) {
+            ok = mbar_wait_warp(&sm.s_full[s_buf], s_ph, ctl, DETAIL_WAIT_ACCFULL);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s);
+            tmem_wait_ld_regs(s);
+          }
+          if (++s_buf == kLdScores) s_buf = 0, s_ph ^= 1;
           const int seen = sees - t * kLdKeys;  // visible keys of this tile
           if (__any_sync(0xFFFFFFFFu, seen < kLdKeys)) {
 #pragma unroll
@@ -376,43 +351,36 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
-          mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // (-inf - -inf is NaN and compares false)
-          grow = mine && t > t_first && (mn - m) * p.scale_log2 > kLdLazy;
-          if (t == t_first) m = mn;
-        }
-        if (named_bar_or(1, 128, grow || !ok)) {
-          // Rare: some row's maximum has grown, or a wait has failed.
-          if (named_bar_or(2, 128, !ok)) {
-            ok = false;
-            break;
-          }
-          if (mine) {
-            const float f = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * p.scale_log2);
+          const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // Rows whose maximum has grown by more than 2^kLdLazy have what they summed so far scaled down;
+          // a segment's first tile has nothing yet. (-inf - -inf is NaN and compares false.)
+          bool grow = mine && (mn - m) * p.scale_log2 > kLdLazy;
+          if (t == t_first) {
             m = mn;
+            grow = false;
+          }
+          const bool any = __any_sync(0xFFFFFFFFu, grow);
+          if (any && mine) {
+            const float f = grow ? exp2_fast((m - mn) * p.scale_log2) : 1.0f;
+            if (grow) m = mn;
             l *= f;
-            sm.fac[row] = f;
+            sm.fac[done % kLdLead][row] = f;
           }
-          named_bar(3, 128);
-          ok = pv_done(done - 1);
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 4 * HT; c += 16) {
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(tO + lanes + c, o);
-            tmem_wait_ld_regs16(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[(c & (HT - 1)) + e]);
-            tmem_st_32x32b_x16(tO + lanes + c, o);
+          if (lane == 0) sm.grow[done % kLdLead][warp] = any;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.m_ready[done % kLdLead]);
+          // The next tile's scores, where they are there already; they arrive behind the exponentials.
+          have = done + 1 < total;
+          if (have) {
+            bool there = false;
+            if (lane == 0) there = mbar_test(&sm.s_full[s_buf], s_ph);
+            have = __shfl_sync(0xFFFFFFFFu, there, 0);
           }
-          tmem_wait_st();
-        }
-        // (The barrier above: S of this tile is complete, so the queries' buffer and, of the tile's rows
-        // behind the request's end, the shared memory may be written.)
-        if (t == te - 1 && left > 0) load_q(next);
-        if (softmax_warp) {
-          // P's half of the buffer is free once the PV of two tiles ago is done.
-          if (done >= 2) ok = pv_done(done - 2) && ok;
+          if (have) {
+            tc_fence_after();
+            tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s_next);
+          }
+          if (done >= 2) ok = pv_done(done - 2);  // P's half of the buffer is free
           if (mine) {
             const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -431,76 +399,159 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             }
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
+          if (have) {
+            tmem_wait_ld_regs(s_next);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = s_next[e];
+          }
+          if (!ok) break;
+        }
+        if (!ok) break;
+        // The segment's sums, once the results of the one before are out.
+        if (seg > 0) ok = mbar_wait_warp(&sm.seg_done, (seg - 1) & 1, ctl, DETAIL_WAIT_ACCEMPTY);
+        if (mine) {
+          if (t_first == 0 && te == nt) {
+            sm.inv[row] = l > 0.0f ? 1.0f / l : 0.0f;
+            if (p.lse && r < R)
+              p.lse[static_cast<int64_t>(b) * R + r] =
+                  l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+          } else {
+            float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
+            ml[row] = m;
+            ml[HT + row] = l;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.seg_ready);
+        ++seg;
+        ++b;
+        t = 0;
+      }
+    }
+    __syncwarp();
+  } else if (total > 0) {
+    // Queries, O^T's scaling and the results (warps 4-7; TMEM quarter warp - 4).
+    const int quarter = warp - 4, ctid = tid - 128;
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0;
+    bool ok = true;
+    // A request's queries into shared memory (zeros behind the last row). A warp takes every fourth row;
+    // a lane finds one of the warp's rows (16 at most) for the others.
+    auto load_q = [&](int b) {
+      const uint16_t* base = p.q + static_cast<int64_t>(b) * p.q_len * p.qs_t;
+      const int rl = ht * HT + quarter + 4 * (lane & 15);
+      const int64_t off = rl < R ? (rl / p.Hq) * p.qs_t + (rl % p.Hq) * p.qs_h : -1;
+#pragma unroll 1
+      for (int k = 0; k < HT / 4; ++k) {
+        const int64_t o = __shfl_sync(0xFFFFFFFFu, off, k);
+        const uint16_t* src = base + (o < 0 ? 0 : o);
+#pragma unroll
+        for (int x = lane; x < kLdDqk / 8; x += 32)
+          cp_async_16(sm.q[x / 8] + sw128(quarter + 4 * k, x & 7), src + (o < 0 ? 0 : x * 8), o < 0 ? 0u : 16u);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+    load_q(b);
+    while (left > 0 && ok) {
+      const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left), t_first = t;
+      left -= te - t;
+      int next = b;                             // the request of the segment after this one
+      if (left > 0) {
+#pragma unroll 1
+        do ++next;
+        while (ld_len(p, next) == 0);
+      }
+#pragma unroll 1
+      for (; t < te; ++t, ++done) {
+        // The tile's scores are complete and read, its rescale factors written.
+        ok = mbar_wait_warp(&sm.m_ready[done % kLdLead], (done / kLdLead) & 1, ctl, DETAIL_WAIT_SCORES);
+        if (!ok) break;
+        const int* grow = sm.grow[done % kLdLead];
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < kSoft; ++w) any |= grow[w] != 0;
+        if (any) {
+          ok = pv_done(done - 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 4 * HT; c += 16) {
+            const int w = (c & (HT - 1)) / 16;  // the softmax warp of these 16 rows
+            if (!grow[w]) continue;
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tO + lanes + c, o);
+            tmem_wait_ld_regs16(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              o[e] = __float_as_uint(__uint_as_float(o[e]) * sm.fac[done % kLdLead][w * 16 + e]);
+            tmem_st_32x32b_x16(tO + lanes + c, o);
+          }
+          tmem_wait_st();
         }
         if ((t + 1) * kLdKeys > n) {
           // Rows behind the request's last key hold anything: zero weights must meet zeros.
-          const int key = tid >> 2;
+          const int key = ctid >> 2;
           if (key >= n - t * kLdKeys)
 #pragma unroll 1
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (2 * (tid & 3) + c) * kLdSlotBytes + key * 128 +
+                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (2 * (ctid & 3) + c) * kLdSlotBytes + key * 128 +
                                           u * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
-        if (++s_buf == kLdScores) s_buf = 0, s_ph ^= 1;
       }
       if (!ok) break;
-      if (left > 0) q_landed();
-      // The segment's result.
-      ok = pv_done(done - 1) && ok;
-      const bool whole = t_first == 0 && te == nt;
-      if (mine) {
-        if (whole) {
-          sm.fac[row] = l > 0.0f ? 1.0f / l : 0.0f;
-          if (p.lse && r < R)
-            p.lse[static_cast<int64_t>(b) * R + r] =
-                l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
-        } else {
-          float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
-          ml[row] = m;
-          ml[HT + row] = l;
-        }
-      }
-      if (!named_bar_and(1, 128, ok)) {
-        ok = false;
-        break;
-      }
+      // Every QK of the segment is done, so the next one's queries may come.
+      if (left > 0) load_q(next);
+      ok = mbar_wait_warp(&sm.seg_ready, seg & 1, ctl, DETAIL_WAIT_SCORES) && pv_done(done - 1);
+      if (!ok) break;
       tc_fence_after();
+      const bool whole = t_first == 0 && te == nt;
       float* part = p.part + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * kLdDv * HT;
 #pragma unroll 1
       for (int c = 0; c < 4 * HT; c += 16) {
         uint32_t o[16];
         tmem_ld_32x32b_x16(tO + lanes + c, o);
         tmem_wait_ld_regs16(o);
-        const int dim = c / HT * 128 + warp * 32 + lane, h0 = c & (HT - 1);
+        const int dim = c / HT * 128 + quarter * 32 + lane, h0 = c & (HT - 1);
         if (whole) {
           uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT + h0) * kLdDv + dim;
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float f = sm.fac[h0 + e];
+            const float f = sm.inv[h0 + e];
             if (ht * HT + h0 + e < R)
               out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[e]) * f) : static_cast<uint16_t>(0);
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(part + dim * HT + h0 + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            *reinterpret_cast<uint4*>(part + (static_cast<int64_t>((h0 + e) / 4) * kLdDv + dim) * 4) =
+                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();
-      named_bar(1, 128);  // fac is read by all before the next segment writes it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.seg_done);
+      ++seg;
       b = next;
       t = 0;
     }
   }
   __syncthreads();
   grid_launch_dependents();
-  if (warp == 5) {
+  if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -514,8 +565,10 @@ constexpr int kLcDims = 64;
 template <int DT, int HT>
 __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, int n_cta) {
   extern __shared__ __align__(16) float lc_smem[];
-  float* wt = lc_smem;                          // [splits][HT]
-  float* tile = lc_smem + n_cta * HT;           // [HT][kLcDims + 1]
+  float* wt = lc_smem;                          // [splits][HT] weights
+  float* ls = wt + n_cta * HT;                  // [splits][HT] sums
+  float* tile = ls + n_cta * HT;                // [HT][kLcDims + 1]
+  __shared__ float inv[HT];
   __shared__ int64_t sh[2];
   const int tid = threadIdx.x, ht = blockIdx.y, d0 = blockIdx.z * kLcDims;
   const int R = p.q_len * p.Hq, rows = min(HT, R - ht * HT);
@@ -546,39 +599,47 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     const int ns = c1 - c0 + 1;
     // The request's first CTA holds its beginning (slot 1), every other one begins inside it (slot 0).
     auto slot = [&](int c) { return (static_cast<int64_t>(ht) * n_cta + c0 + c) * 2 + (c == 0 ? 1 : 0); };
+    // The splits' m into the weights' place and their l behind, then one thread a row.
+    for (int i = tid; i < ns * HT; i += 256) {
+      const float* ml = p.ml + slot(i / HT) * 2 * HT + i % HT;
+      wt[i] = ml[0];
+      ls[i] = ml[HT];
+    }
+    __syncthreads();
     if (tid < HT) {
       float M = -INFINITY, L = 0.0f;
-      for (int c = 0; c < ns; ++c) M = fmaxf(M, p.ml[slot(c) * 2 * HT + tid]);
+#pragma unroll 4
+      for (int c = 0; c < ns; ++c) M = fmaxf(M, wt[c * HT + tid]);
+#pragma unroll 4
       for (int c = 0; c < ns; ++c) {
-        const float mc = p.ml[slot(c) * 2 * HT + tid];
-        const float w = mc == -INFINITY ? 0.0f : exp2f((mc - M) * p.scale_log2);
+        const float mc = wt[c * HT + tid], w = mc == -INFINITY ? 0.0f : exp2f((mc - M) * p.scale_log2);
         wt[c * HT + tid] = w;
-        L += w * p.ml[slot(c) * 2 * HT + HT + tid];
+        L += w * ls[c * HT + tid];
       }
-      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-      for (int c = 0; c < ns; ++c) wt[c * HT + tid] *= inv;
+      inv[tid] = L > 0.0f ? 1.0f / L : 0.0f;
       if (lse && blockIdx.z == 0 && tid < rows)
         lse[tid] = L > 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
     }
     __syncthreads();
-    constexpr int kVecs = kLcDims * HT / 4;     // float4s of the block's dims
-#pragma unroll
+    constexpr int kVecs = kLcDims * HT / 4;     // float4s (four rows of a dim) of the block's dims
+#pragma unroll 1
     for (int v = tid; v < kVecs; v += 256) {
-      const int dim = v / (HT / 4), h = v % (HT / 4) * 4;
+      const int dim = v % kLcDims, h = v / kLcDims * 4;
+      const float* src = p.part + (static_cast<int64_t>(h / 4) * kLdDv + d0 + dim) * 4;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
       for (int c = 0; c < ns; ++c) {
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(p.part + (slot(c) * kLdDv + d0 + dim) * HT + h));
+        const float4 o = __ldcs(reinterpret_cast<const float4*>(src + slot(c) * kLdDv * HT));
         const float4 w = *reinterpret_cast<const float4*>(wt + c * HT + h);
         acc.x += w.x * o.x;
         acc.y += w.y * o.y;
         acc.z += w.z * o.z;
         acc.w += w.w * o.w;
       }
-      tile[(h + 0) * (kLcDims + 1) + dim] = acc.x;
-      tile[(h + 1) * (kLcDims + 1) + dim] = acc.y;
-      tile[(h + 2) * (kLcDims + 1) + dim] = acc.z;
-      tile[(h + 3) * (kLcDims + 1) + dim] = acc.w;
+      tile[(h + 0) * (kLcDims + 1) + dim] = acc.x * inv[h];
+      tile[(h + 1) * (kLcDims + 1) + dim] = acc.y * inv[h + 1];
+      tile[(h + 2) * (kLcDims + 1) + dim] = acc.z * inv[h + 2];
+      tile[(h + 3) * (kLcDims + 1) + dim] = acc.w * inv[h + 3];
     }
     __syncthreads();
     for (int i = tid; i < rows * kLcDims / 2; i += 256) {
@@ -618,7 +679,7 @@ static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t str
                    part + static_cast<size_t>(row_tiles) * n_cta * 2 * kLdDv * HT, a.hdr, a.budget_ns};
   const size_t smem = sizeof(LdSmem<HT>) + 1024;
   static_assert(sizeof(LdSmem<HT>) + 1024 <= 227 * 1024, "shared memory");
-  const size_t csmem = (static_cast<size_t>(n_cta) * HT + HT * (kLcDims + 1)) * sizeof(float);
+  const size_t csmem = (2 * static_cast<size_t>(n_cta) * HT + HT * (kLcDims + 1)) * sizeof(float);
   if (cudaFuncSetAttribute(latent_decode_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess ||
       cudaFuncSetAttribute(latent_combine_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
