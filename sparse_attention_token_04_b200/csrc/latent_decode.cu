@@ -147,13 +147,19 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         const int n = __ldg(&p.seq_lens[b]);
         if (n < 0 || n > p.max_blocks * p.block_size) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SEQ_LEN);
       }
-    const int64_t T = ld_tiles_before(p, p.B, lane);
+    const int nt0 = lane < p.B ? ld_tiles(p, lane) : 0;  // (of the first 32 requests)
+    int64_t T = nt0;
+#pragma unroll 1
+    for (int b = lane + 32; b < p.B; b += 32) T += ld_tiles(p, b);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) T += __shfl_xor_sync(0xFFFFFFFFu, T, off);
     const int64_t G = ld_sharers(T, gridDim.y);
     const int64_t lo = cta < G ? T * cta / G : T, hi = cta < G ? T * (cta + 1) / G : T;
     int64_t carry = 0;
+#pragma unroll 1
     for (int base = 0; base < p.B && lo < hi; base += 32) {
       const int bb = base + lane;
-      const int nt = bb < p.B ? ld_tiles(p, bb) : 0;
+      const int nt = base == 0 ? nt0 : bb < p.B ? ld_tiles(p, bb) : 0;
       int incl = nt;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -521,24 +527,29 @@ __global__ void __launch_bounds__(kLdThreads, 1)
       const bool whole = t_first == 0 && te == nt;
       float* part = p.part + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * kLdDv * HT;
 #pragma unroll 1
-      for (int c = 0; c < 4 * HT; c += 16) {
-        uint32_t o[16];
-        tmem_ld_32x32b_x16(tO + lanes + c, o);
-        tmem_wait_ld_regs16(o);
-        const int dim = c / HT * 128 + quarter * 32 + lane, h0 = c & (HT - 1);
-        if (whole) {
-          uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT + h0) * kLdDv + dim;
+      for (int c = 0; c < 4 * HT; c += 32) {    // 16 columns at a time, two loads in flight
+        uint32_t o[2][16];
+        tmem_ld_32x32b_x16(tO + lanes + c, o[0]);
+        tmem_ld_32x32b_x16(tO + lanes + c + 16, o[1]);
+        tmem_wait_ld_regs16(o[0]);
+        tmem_wait_ld_regs16(o[1]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float f = sm.inv[h0 + e];
-            if (ht * HT + h0 + e < R)
-              out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[e]) * f) : static_cast<uint16_t>(0);
+        for (int k = 0; k < 2; ++k) {
+          const int col = c + 16 * k, dim = col / HT * 128 + quarter * 32 + lane, h0 = col & (HT - 1);
+          if (whole) {
+            uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT + h0) * kLdDv + dim;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float f = sm.inv[h0 + e];
+              if (ht * HT + h0 + e < R)
+                out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[k][e]) * f) : static_cast<uint16_t>(0);
+            }
+          } else {
+            float* dst = part + (static_cast<int64_t>(h0 / 4) * kLdDv + dim) * 4;
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<uint4*>(dst + e * kLdDv) = make_uint4(o[k][e], o[k][e + 1], o[k][e + 2], o[k][e + 3]);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<uint4*>(part + (static_cast<int64_t>((h0 + e) / 4) * kLdDv + dim) * 4) =
-                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       tc_fence_before();
@@ -559,18 +570,22 @@ __global__ void __launch_bounds__(kLdThreads, 1)
 
 // Joins the split requests: with M the largest m_c of a row, out = sum_c 2^((m_c - M) scale log2 e) O_c
 // / L, L the same sum of the l_c, lse = scale M + ln L. A request without keys gets zeros and -inf.
-// Block (x, ht, z) takes 64 of the dims of a run of requests; the partial sums are read along the
-// rows (as they were written) and turned in shared memory so that out is written along the dims.
-constexpr int kLcDims = 64;
+// Block (x, ht, z) takes kLcDims of the dims of a run of requests, four rows of one dim a thread; the
+// partial sums are read along the dims and turned in shared memory, so that out is written along them
+// too.
+template <int HT>
+struct Lc {
+  static constexpr int kDims = 256 * 4 / HT;    // 16 (HT = 64) to 64 (HT = 16): a vector a thread
+  static constexpr int kPitch = kDims + 2;
+};
 template <int DT, int HT>
 __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, int n_cta) {
+  constexpr int kDims = Lc<HT>::kDims, kPitch = Lc<HT>::kPitch, kPer = 256 / HT;  // kPer: threads of a row
   extern __shared__ __align__(16) float lc_smem[];
   float* wt = lc_smem;                          // [splits][HT] weights
-  float* ls = wt + n_cta * HT;                  // [splits][HT] sums
-  float* tile = ls + n_cta * HT;                // [HT][kLcDims + 1]
-  __shared__ float inv[HT];
+  float* tile = lc_smem + n_cta * HT;           // [HT][kPitch]
   __shared__ int64_t sh[2];
-  const int tid = threadIdx.x, ht = blockIdx.y, d0 = blockIdx.z * kLcDims;
+  const int tid = threadIdx.x, ht = blockIdx.y, d0 = blockIdx.z * kDims;
   const int R = p.q_len * p.Hq, rows = min(HT, R - ht * HT);
   const int b_lo = static_cast<int>(static_cast<int64_t>(p.B) * blockIdx.x / gridDim.x);
   const int b_hi = static_cast<int>(static_cast<int64_t>(p.B) * (blockIdx.x + 1) / gridDim.x);
@@ -589,7 +604,7 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT) * kLdDv + d0;
     float* lse = p.lse ? p.lse + static_cast<int64_t>(b) * R + ht * HT : nullptr;
     if (nt == 0) {
-      for (int i = tid; i < rows * kLcDims; i += 256) out[(i / kLcDims) * kLdDv + i % kLcDims] = 0;
+      for (int i = tid; i < rows * kDims; i += 256) out[(i / kDims) * kLdDv + i % kDims] = 0;
       if (lse && blockIdx.z == 0 && tid < rows) lse[tid] = -INFINITY;
       continue;
     }
@@ -598,36 +613,38 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     if (c0 == c1) continue;
     const int ns = c1 - c0 + 1;
     // The request's first CTA holds its beginning (slot 1), every other one begins inside it (slot 0).
-    auto slot = [&](int c) { return (static_cast<int64_t>(ht) * n_cta + c0 + c) * 2 + (c == 0 ? 1 : 0); };
-    // The splits' m into the weights' place and their l behind, then one thread a row.
-    for (int i = tid; i < ns * HT; i += 256) {
-      const float* ml = p.ml + slot(i / HT) * 2 * HT + i % HT;
-      wt[i] = ml[0];
-      ls[i] = ml[HT];
-    }
-    __syncthreads();
-    if (tid < HT) {
+    const int64_t slot0 = (static_cast<int64_t>(ht) * n_cta + c0) * 2;
+    auto slot = [&](int c) { return slot0 + 2 * c + (c == 0 ? 1 : 0); };
+    {
+      const int row = tid / kPer, c_first = tid % kPer;
       float M = -INFINITY, L = 0.0f;
 #pragma unroll 4
-      for (int c = 0; c < ns; ++c) M = fmaxf(M, wt[c * HT + tid]);
-#pragma unroll 4
-      for (int c = 0; c < ns; ++c) {
-        const float mc = wt[c * HT + tid], w = mc == -INFINITY ? 0.0f : exp2f((mc - M) * p.scale_log2);
-        wt[c * HT + tid] = w;
-        L += w * ls[c * HT + tid];
+      for (int c = c_first; c < ns; c += kPer) {
+        const float mc = p.ml[slot(c) * 2 * HT + row];
+        wt[c * HT + row] = mc;
+        M = fmaxf(M, mc);
       }
-      inv[tid] = L > 0.0f ? 1.0f / L : 0.0f;
-      if (lse && blockIdx.z == 0 && tid < rows)
-        lse[tid] = L > 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+#pragma unroll
+      for (int off = 1; off < kPer; off *= 2) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+#pragma unroll 4
+      for (int c = c_first; c < ns; c += kPer) {
+        const float mc = wt[c * HT + row], w = mc == -INFINITY ? 0.0f : exp2f((mc - M) * p.scale_log2);
+        wt[c * HT + row] = w;
+        L += w * p.ml[slot(c) * 2 * HT + HT + row];
+      }
+#pragma unroll
+      for (int off = 1; off < kPer; off *= 2) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      for (int c = c_first; c < ns; c += kPer) wt[c * HT + row] *= inv;
+      if (lse && blockIdx.z == 0 && c_first == 0 && row < rows)
+        lse[row] = L > 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
     }
     __syncthreads();
-    constexpr int kVecs = kLcDims * HT / 4;     // float4s (four rows of a dim) of the block's dims
-#pragma unroll 1
-    for (int v = tid; v < kVecs; v += 256) {
-      const int dim = v % kLcDims, h = v / kLcDims * 4;
+    {
+      const int dim = tid % kDims, h = tid / kDims * 4;
       const float* src = p.part + (static_cast<int64_t>(h / 4) * kLdDv + d0 + dim) * 4;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
       for (int c = 0; c < ns; ++c) {
         const float4 o = __ldcs(reinterpret_cast<const float4*>(src + slot(c) * kLdDv * HT));
         const float4 w = *reinterpret_cast<const float4*>(wt + c * HT + h);
@@ -636,16 +653,15 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
         acc.z += w.z * o.z;
         acc.w += w.w * o.w;
       }
-      tile[(h + 0) * (kLcDims + 1) + dim] = acc.x * inv[h];
-      tile[(h + 1) * (kLcDims + 1) + dim] = acc.y * inv[h + 1];
-      tile[(h + 2) * (kLcDims + 1) + dim] = acc.z * inv[h + 2];
-      tile[(h + 3) * (kLcDims + 1) + dim] = acc.w * inv[h + 3];
+      tile[(h + 0) * kPitch + dim] = acc.x;
+      tile[(h + 1) * kPitch + dim] = acc.y;
+      tile[(h + 2) * kPitch + dim] = acc.z;
+      tile[(h + 3) * kPitch + dim] = acc.w;
     }
     __syncthreads();
-    for (int i = tid; i < rows * kLcDims / 2; i += 256) {
-      const int h = i / (kLcDims / 2), d = i % (kLcDims / 2) * 2;
-      *reinterpret_cast<uint32_t*>(out + h * kLdDv + d) =
-          ld_pack<DT>(tile[h * (kLcDims + 1) + d], tile[h * (kLcDims + 1) + d + 1]);
+    for (int i = tid; i < rows * kDims / 2; i += 256) {
+      const int h = i / (kDims / 2), d = i % (kDims / 2) * 2;
+      *reinterpret_cast<uint32_t*>(out + h * kLdDv + d) = ld_pack<DT>(tile[h * kPitch + d], tile[h * kPitch + d + 1]);
     }
     __syncthreads();
   }
@@ -679,7 +695,7 @@ static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t str
                    part + static_cast<size_t>(row_tiles) * n_cta * 2 * kLdDv * HT, a.hdr, a.budget_ns};
   const size_t smem = sizeof(LdSmem<HT>) + 1024;
   static_assert(sizeof(LdSmem<HT>) + 1024 <= 227 * 1024, "shared memory");
-  const size_t csmem = (2 * static_cast<size_t>(n_cta) * HT + HT * (kLcDims + 1)) * sizeof(float);
+  const size_t csmem = (static_cast<size_t>(n_cta) * HT + HT * Lc<HT>::kPitch) * sizeof(float);
   if (cudaFuncSetAttribute(latent_decode_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess ||
       cudaFuncSetAttribute(latent_combine_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -691,7 +707,7 @@ static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t str
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(std::min(a.B, 128), row_tiles, kLdDv / kLcDims);
+  cfg.gridDim = dim3(std::min(a.B, 128), row_tiles, kLdDv / Lc<HT>::kDims);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = csmem;
   cfg.stream = stream;
