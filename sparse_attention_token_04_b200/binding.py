@@ -507,6 +507,7 @@ def dsa_sparse_attention_decode(q, latent, block_table, seq_lens, idx, scale: fl
 
 
 _DTYPES = {torch.bfloat16: DSA_DTYPE_BF16, torch.float16: DSA_DTYPE_F16, torch.float32: DSA_DTYPE_F32}
+_HALF = (torch.bfloat16, torch.float16)
 
 
 def _rows(t, name: str, dtypes, shape) -> None:
@@ -515,7 +516,7 @@ def _rows(t, name: str, dtypes, shape) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -526,36 +527,45 @@ def _st(t, i: int) -> int:
     return t.stride(i) if t.shape[i] > 1 else 8
 
 
-class _On:
-    """Makes `device` (every tensor's) current and, where a stream other than the current one is
-    given, that stream too, so that what the call allocates belongs to the stream that uses it."""
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, stream, first: torch.Tensor, *others):
-        for t in others:
-            if t is not None and t.device != first.device:
-                raise ValueError(f"tensors on {first.device} and {t.device}")
-        self.device, self.stream, self.held = first.device, stream, []
 
-    def __enter__(self):
-        if self.device.index != torch.cuda.current_device():
-            self._hold(torch.cuda.device(self.device))
-        now = torch.cuda.current_stream()
-        if self.stream is None:
-            return ctypes.c_void_p(now.cuda_stream)
-        raw = int(self.stream.cuda_stream if hasattr(self.stream, "cuda_stream") else self.stream)
-        if raw != now.cuda_stream:
-            other = self.stream if isinstance(self.stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw)
-            self._hold(torch.cuda.stream(other))
-        return ctypes.c_void_p(raw)
+# The current stream's handle without a Stream object around it, which takes longer to make than a
+# small call's launch.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-    def _hold(self, ctx):
-        ctx.__enter__()
-        self.held.append(ctx)
 
-    def __exit__(self, *exc):
-        while self.held:
-            self.held.pop().__exit__(*exc)
-        return False
+def _leave(held) -> None:
+    while held:
+        held.pop().__exit__(None, None, None)
+
+
+def _enter(stream, first: torch.Tensor, *others):
+    """Makes the device of `first` (every tensor's) current and, where a stream other than the current
+    one is given, that stream too, so that what the call allocates belongs to the stream that uses it.
+    Returns (the stream's handle, contexts for _leave)."""
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    held = []
+    if device != torch.cuda.current_device():
+        held.append(torch.cuda.device(device))
+        held[-1].__enter__()
+    now = _raw_stream(device)
+    if stream is None:
+        return now, held
+    raw = int(stream.cuda_stream if hasattr(stream, "cuda_stream") else stream)
+    if raw != now:
+        if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+            _leave(held)
+            raise ValueError(f"a stream of device {stream.device_index} for tensors on {first.device}")
+        held.append(torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                                      else torch.cuda.ExternalStream(raw, device=device)))
+        held[-1].__enter__()
+    return raw, held
 
 
 def _rotation(T: int, d: int, positions, inv_freq):
@@ -595,13 +605,17 @@ def dsa_rotary(x, positions, inv_freq, interleaved: bool = False, rot_offset: in
     rot = _rotation(T, d, positions, inv_freq)
     if rot == 0:
         raise ValueError("positions and inv_freq are needed")
-    with _On(stream, x, positions, inv_freq, out) as s:
+    s, held = _enter(stream, x, positions, inv_freq, out)
+    try:
         if out is None:
             out = torch.empty(T, H, d, dtype=x.dtype, device=x.device)
-        _rows(out, "out", (x.dtype,), (T, H, d))
-        _check(lib().dsa_rotary(_ptr(x), _st(x, 0), _st(x, 1), _ptr(positions), _ptr(inv_freq), T, H, d, rot,
+        else:
+            _rows(out, "out", (x.dtype,), (T, H, d))
+        _check(lib().dsa_rotary(_addr(x), _st(x, 0), _st(x, 1), _addr(positions), _addr(inv_freq), T, H, d, rot,
                                 int(rot_offset), int(interleaved), int(inverse), float(mscale), _DTYPES[x.dtype],
-                                _ptr(out), _st(out, 0), _st(out, 1), s), "dsa_rotary")
+                                _addr(out), _st(out, 0), _st(out, 1), s), "dsa_rotary")
+    finally:
+        _leave(held)
     return out
 
 
@@ -615,18 +629,23 @@ def dsa_index_quantise(x, positions=None, inv_freq=None, interleaved: bool = Fal
     H = int(x.shape[1]) if x.dim() == 3 else 1
     _rows(x, "x", _DTYPES, x.shape)
     rot = _rotation(T, d, positions, inv_freq)
-    with _On(stream, x, positions, inv_freq, codes, scale, workspace) as s:
+    s, held = _enter(stream, x, positions, inv_freq, codes, scale, workspace)
+    try:
         if codes is None:
             codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-        _need(codes, "codes", torch.uint8, x.shape)
+        else:
+            _need(codes, "codes", torch.uint8, x.shape)
         if scale is None:
             scale = torch.empty(T, dtype=torch.float32, device=x.device)
-        _need(scale, "scale", torch.float32, (T,))
-        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s.value or 0)
-        _check(lib().dsa_index_quantise(_ptr(x), _st(x, 0), _st(x, 1) if x.dim() == 3 else 8, T, H, d,
-                                        _DTYPES[x.dtype], _ptr(positions), _ptr(inv_freq), rot, int(rot_offset),
-                                        int(interleaved), float(mscale), _ptr(codes), _ptr(scale), _ptr(ws),
+        else:
+            _need(scale, "scale", torch.float32, (T,))
+        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s)
+        _check(lib().dsa_index_quantise(_addr(x), _st(x, 0), _st(x, 1) if x.dim() == 3 else 8, T, H, d,
+                                        _DTYPES[x.dtype], _addr(positions), _addr(inv_freq), rot, int(rot_offset),
+                                        int(interleaved), float(mscale), _addr(codes), _addr(scale), _addr(ws),
                                         ws.numel(), s), "dsa_index_quantise")
+    finally:
+        _leave(held)
     return codes, scale
 
 
@@ -644,14 +663,15 @@ def dsa_index_cache_write(x, slots, k_cache, k_scale_cache, positions=None, inv_
     _need(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
     _need(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
     rot = _rotation(T, d, positions, inv_freq)
-    with _On(stream, x, slots, k_cache, k_scale_cache, positions, inv_freq, workspace) as s:
-        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s.value or 0)
-        _check(lib().dsa_index_cache_write(_ptr(x), _st(x, 0), T, d, _DTYPES[x.dtype], _ptr(slots), _ptr(positions),
-                                           _ptr(inv_freq), rot, int(rot_offset), int(interleaved), float(mscale),
-                                           _ptr(k_cache), _ptr(k_scale_cache), n_blocks, block_size, _ptr(ws),
+    s, held = _enter(stream, x, slots, k_cache, k_scale_cache, positions, inv_freq, workspace)
+    try:
+        ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s)
+        _check(lib().dsa_index_cache_write(_addr(x), _st(x, 0), T, d, _DTYPES[x.dtype], _addr(slots), _addr(positions),
+                                           _addr(inv_freq), rot, int(rot_offset), int(interleaved), float(mscale),
+                                           _addr(k_cache), _addr(k_scale_cache), n_blocks, block_size, _addr(ws),
                                            ws.numel(), s), "dsa_index_cache_write")
-
-
+    finally:
+        _leave(held)
 def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: int, starts=None,
                          want_codes: bool = True, values=None, out_codes=None, out_scale=None, out_values=None,
                          workspace=None, stream=None):
@@ -672,8 +692,9 @@ def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: in
     if values is not None and values not in _DTYPES:
         raise ValueError(f"values must be one of {[str(t) for t in _DTYPES]}, got {values}")
     dev = k_cache.device
-    with _On(stream, k_cache, k_scale_cache, block_table, cu_rows, starts, out_codes, out_scale, out_values,
-             workspace) as s:
+    s, held = _enter(stream, k_cache, k_scale_cache, block_table, cu_rows, starts, out_codes, out_scale,
+                      out_values, workspace)
+    try:
         if want_codes and out_codes is None:
             out_codes = torch.empty(total, d, dtype=torch.uint8, device=dev)
         if want_codes and out_scale is None:
@@ -686,12 +707,14 @@ def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: in
             _need(out_scale, "out_scale", torch.float32, (total,))
         if out_values is not None:
             _need(out_values, "out_values", values, (total, d))
-        ws = _workspace(DSA_WS_HEADER_BYTES, dev, workspace, s.value or 0)
-        _check(lib().dsa_index_cache_read(_ptr(k_cache), _ptr(k_scale_cache), n_blocks, block_size, d,
-                                          _ptr(block_table), int(block_table.shape[1]), _ptr(starts), _ptr(cu_rows),
-                                          B, total, _ptr(out_codes), _ptr(out_scale), _ptr(out_values),
-                                          _DTYPES.get(values, DSA_DTYPE_F32), _ptr(ws), ws.numel(), s),
+        ws = _workspace(DSA_WS_HEADER_BYTES, dev, workspace, s)
+        _check(lib().dsa_index_cache_read(_addr(k_cache), _addr(k_scale_cache), n_blocks, block_size, d,
+                                          _addr(block_table), int(block_table.shape[1]), _addr(starts), _addr(cu_rows),
+                                          B, total, _addr(out_codes), _addr(out_scale), _addr(out_values),
+                                          _DTYPES.get(values, DSA_DTYPE_F32), _addr(ws), ws.numel(), s),
                "dsa_index_cache_read")
+    finally:
+        _leave(held)
     return out_codes, out_scale, out_values
 
 
@@ -709,8 +732,7 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
         raise ValueError("q must be a tensor of shape (B, q_len, Hq, 576) or (B, Hq, 576)")
     q4 = q if q.dim() == 4 else q[:, None]
     B, q_len, Hq, dqk = (int(n) for n in q4.shape)
-    half = (torch.bfloat16, torch.float16)
-    _rows(q, "q", half, q.shape)
+    _rows(q, "q", _HALF, q.shape)
     if B > 1 and q_len > 1 and q4.stride(0) != q_len * q4.stride(1):
         raise ValueError("q's tokens must be evenly spaced over its requests")
     q_stride_t = _st(q4, 1) if q_len > 1 else _st(q4, 0)
@@ -720,20 +742,24 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     _need(seq_lens, "seq_lens", torch.int32, (B,))
     if block_size < 1 or n_rows % block_size:
         raise ValueError("latent rows must be whole blocks")
-    with _On(stream, q, latent, block_table, seq_lens, out, lse, workspace) as s:
+    s, held = _enter(stream, q, latent, block_table, seq_lens, out, lse, workspace)
+    try:
         if out is None:
             out = torch.empty(q.shape[:-1] + (dv,), dtype=q.dtype, device=q.device)
-        _need(out, "out", q.dtype, q.shape[:-1] + (dv,))
+        else:
+            _need(out, "out", q.dtype, q.shape[:-1] + (dv,))
         if lse is None and want_lse:
             lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-        if lse is not None:
+        elif lse is not None:
             _need(lse, "lse", torch.float32, q.shape[:-1])
-        ws = _workspace(dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq), q.device, workspace, s.value or 0)
-        _check(lib().dsa_latent_attention_decode(_ptr(q), q_stride_t, _st(q4, 2), _ptr(latent), n_rows // block_size,
-                                                 block_size, _ptr(block_table), int(block_table.shape[1]),
-                                                 _ptr(seq_lens), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], float(scale),
-                                                 _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s),
+        ws = _workspace(dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq), q.device, workspace, s)
+        _check(lib().dsa_latent_attention_decode(_addr(q), q_stride_t, _st(q4, 2), _addr(latent), n_rows // block_size,
+                                                 block_size, _addr(block_table), int(block_table.shape[1]),
+                                                 _addr(seq_lens), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], float(scale),
+                                                 _addr(out), _addr(lse), _addr(ws), ws.numel(), s),
                "dsa_latent_attention_decode")
+    finally:
+        _leave(held)
     return out, lse
 
 
@@ -745,8 +771,7 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor of shape (Tq, H, 192)")
     Tq, H, dqk = (int(n) for n in q.shape)
-    half = (torch.bfloat16, torch.float16)
-    _rows(q, "q", half, (Tq, H, dqk))
+    _rows(q, "q", _HALF, (Tq, H, dqk))
     Tk, d_nope, d_pe, dv = int(k_pe.shape[0]), int(k_nope.shape[-1]), int(k_pe.shape[-1]), int(v.shape[-1])
     _rows(k_nope, "k_nope", (q.dtype,), (Tk, H, d_nope))
     _rows(k_pe, "k_pe", (q.dtype,), (Tk, d_pe))
@@ -755,18 +780,22 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
         raise ValueError("q's heads must be as wide as k_nope's and k_pe together")
     _need(cu_q, "cu_q", torch.int32)
     _need(cu_k, "cu_k", torch.int32, cu_q.shape)
-    with _On(stream, q, k_nope, k_pe, v, cu_q, cu_k, out, lse, workspace) as s:
+    s, held = _enter(stream, q, k_nope, k_pe, v, cu_q, cu_k, out, lse, workspace)
+    try:
         if out is None:
             out = torch.empty(Tq, H, dv, dtype=q.dtype, device=q.device)
-        _need(out, "out", q.dtype, (Tq, H, dv))
+        else:
+            _need(out, "out", q.dtype, (Tq, H, dv))
         if lse is None and want_lse:
             lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
-        if lse is not None:
+        elif lse is not None:
             _need(lse, "lse", torch.float32, (Tq, H))
-        ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s.value or 0)
+        ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s)
         _check(lib().dsa_latent_attention_prefill(
-            _ptr(q), _st(q, 0), _st(q, 1), _ptr(k_nope), _st(k_nope, 0), _st(k_nope, 1), _ptr(k_pe),
-            _st(k_pe, 0), _ptr(v), _st(v, 0), _st(v, 1), _ptr(cu_q), _ptr(cu_k), int(cu_q.numel()) - 1, Tq, Tk,
-            int(max_q), H, d_nope, d_pe, dv, _DTYPES[q.dtype], int(causal), float(scale), _ptr(out), _ptr(lse),
-            _ptr(ws), ws.numel(), s), "dsa_latent_attention_prefill")
+            _addr(q), _st(q, 0), _st(q, 1), _addr(k_nope), _st(k_nope, 0), _st(k_nope, 1), _addr(k_pe),
+            _st(k_pe, 0), _addr(v), _st(v, 0), _st(v, 1), _addr(cu_q), _addr(cu_k), int(cu_q.numel()) - 1, Tq, Tk,
+            int(max_q), H, d_nope, d_pe, dv, _DTYPES[q.dtype], int(causal), float(scale), _addr(out), _addr(lse),
+            _addr(ws), ws.numel(), s), "dsa_latent_attention_prefill")
+    finally:
+        _leave(held)
     return out, lse

@@ -15,8 +15,14 @@
 
 namespace dsa {
 
-constexpr int kQuantThreads = 256;
-constexpr int kQuantItems = kQuantMaxRow / kItem / kQuantThreads;  // items a thread holds, at most
+constexpr int kQuantThreads = 128;
+
+// Whether a quotient y of magnitude >= 2^-6 lies within four ulps of a border between two codes (their
+// middle: the mantissa bits behind E4M3's three are 1000...).
+__device__ __forceinline__ bool near_border(float y) {
+  const uint32_t u = __float_as_uint(y);
+  return ((u + 4u) & 0xFFFFFu) - 0x80000u <= 8u;
+}
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -24,21 +30,27 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (hi << 16);
 }
 
-// NaN counts as 0 and an infinity as the largest fp32 value of its sign; true if v was not finite.
-__device__ __forceinline__ bool make_finite(float& v) {
-  if (fabsf(v) <= FLT_MAX) return false;
-  v = isnan(v) ? 0.0f : copysignf(FLT_MAX, v);
-  return true;
+// NaN counts as 0 and an infinity as the largest fp32 value of its sign.
+__device__ __forceinline__ float finite(float v) {
+  if (fabsf(v) <= FLT_MAX) return v;
+  return isnan(v) ? 0.0f : copysignf(FLT_MAX, v);
+}
+// The larger of two non-negative values, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
 }
 
-// G threads of a CTA take one row (G a power of two, 8 to 256), so a CTA takes 256 / G rows. G is
-// the number of items of a row where that is at most 32 (one warp then holds whole rows and needs
-// no barrier for their maxima), else all 256 threads.
-template <int DT, int G>
-__global__ void __launch_bounds__(kQuantThreads) index_quantise_kernel(const QuantParams p) {
+// G threads of a CTA take one row of up to NI * G items, so a CTA takes 128 / G rows: short rows (up to
+// 32 items) one item a thread, so that one warp holds whole rows and needs no barrier for their maxima,
+// others all 128 threads. The values stay packed as they were loaded (every load of a row is in flight
+// at once, and six CTAs fit an SM) and are rotated twice, for the maximum and for the codes. (As fp32
+// with 256 threads, two CTAs an SM: 301 us for 16384 x 64 x 128 bf16 values, against a floor of 62.)
+template <int DT, int G, int NI>
+__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) index_quantise_kernel(const QuantParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kRows = kQuantThreads / G;
-  constexpr int NI = G == kQuantThreads ? kQuantItems : 1;
   extern __shared__ float2 cs_all[];
   __shared__ float warp_max[kQuantThreads / 32];
   const int half = p.r.rot / 2;
@@ -53,16 +65,19 @@ __global__ void __launch_bounds__(kQuantThreads) index_quantise_kernel(const Qua
       dst = -1;
     }
   }
-  float a[NI][kVec], b[NI][kVec];
+  // i / per_head for i < 1024 (per_head_inv = ceil(2^20 / per_head)).
+  auto head_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * p.per_head_inv) >> 20); };
+  RawVec<DT> ra[NI], rb[NI];
   const T* row = static_cast<const T*>(p.x) + t * p.xs_t;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
     const int i = l + k * G;
     if (dst < 0 || i >= n) continue;
-    const Item it = rotary_item(i % per_head, p.r);
-    const T* h = row + (i / per_head) * p.xs_h;
-    load_vec<DT>(h + it.a, a[k]);
-    load_vec<DT>(h + it.b, b[k]);
+    const int head = head_of(i);
+    const Item it = rotary_item(i - head * per_head, p.r);
+    const T* h = row + head * p.xs_h;
+    ra[k] = load_raw<DT>(h + it.a);
+    rb[k] = load_raw<DT>(h + it.b);
   }
   for (int i = threadIdx.x; i < kRows * half; i += kQuantThreads) {
     const int64_t tt = t0 + i / half;
@@ -70,69 +85,103 @@ __global__ void __launch_bounds__(kQuantThreads) index_quantise_kernel(const Qua
   }
   __syncthreads();
   float top = 0.0f;
-  bool bad = false;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
     const int i = l + k * G;
     if (dst < 0 || i >= n) continue;
-    rotary_turn(rotary_item(i % per_head, p.r), p.r, cs_all + g * half, a[k], b[k]);
+    float a[kVec], b[kVec];
+    unpack_raw<DT>(ra[k], a);
+    unpack_raw<DT>(rb[k], b);
+    rotary_turn(rotary_item(i - head_of(i) * per_head, p.r), p.r, cs_all + g * half, a, b);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      bad |= make_finite(a[k][e]) | make_finite(b[k][e]);
-      top = fmaxf(top, fmaxf(fabsf(a[k][e]), fabsf(b[k][e])));
-    }
+    for (int e = 0; e < kVec; ++e) top = max_or_nan(top, max_or_nan(fabsf(a[e]), fabsf(b[e])));
   }
-  if (bad) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_NOT_FINITE);
 #pragma unroll
   for (int off = (G < 32 ? G : 32) / 2; off > 0; off >>= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
   if constexpr (G > 32) {
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < G / 32; ++w) top = fmaxf(top, warp_max[(threadIdx.x & ~(G - 1)) / 32 + w]);
+    for (int w = 0; w < G / 32; ++w) top = max_or_nan(top, warp_max[w]);
   }
   if (dst < 0) return;
+  // A row with a value that is not finite: its maximum is not finite either, and is taken over the others.
+  const bool mend = !(top <= FLT_MAX);
+  if (mend) {
+    if (l == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_NOT_FINITE);
+    top = 0.0f;
+    for (int i = 0; i < n; ++i) {  // (every thread goes through the whole row: it is a bad one)
+      const int head = head_of(i);
+      const Item it = rotary_item(i - head * per_head, p.r);
+      float a[kVec], b[kVec];
+      load_vec<DT>(row + head * p.xs_h + it.a, a);
+      load_vec<DT>(row + head * p.xs_h + it.b, b);
+      rotary_turn(it, p.r, cs_all + g * half, a, b);
+#pragma unroll 1
+      for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaxf(fabsf(finite(a[e])), fabsf(finite(b[e]))));
+    }
+  }
   const float scale = top > 0.0f ? fmaxf(__fdiv_rn(top, 448.0f), FLT_MIN) : 1.0f;
+  // The product with the rounded reciprocal is within two ulps of the quotient. It has the quotient's
+  // code unless it is that close to a border between codes or, where the codes' steps no longer scale
+  // with the value, below 2^-6: the item is then divided, a few in a hundred.
+  const float inv = __fdiv_rn(1.0f, scale);
   uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d);
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
     const int i = l + k * G;
     if (i >= n) continue;
-    const Item it = rotary_item(i % per_head, p.r);
-    uint8_t* h = out + (i / per_head) * p.d;
+    const int head = head_of(i);
+    const Item it = rotary_item(i - head * per_head, p.r);
+    float v[2][kVec], y[2][kVec];
+    unpack_raw<DT>(ra[k], v[0]);
+    unpack_raw<DT>(rb[k], v[1]);
+    rotary_turn(it, p.r, cs_all + g * half, v[0], v[1]);
+    bool divide = mend;
+    float least = INFINITY;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      a[k][e] = __fdiv_rn(a[k][e], scale);
-      b[k][e] = __fdiv_rn(b[k][e], scale);
+    for (int e = 0; e < 2 * kVec; ++e) {
+      y[e / kVec][e % kVec] = v[e / kVec][e % kVec] * inv;
+      divide |= near_border(y[e / kVec][e % kVec]);
+      least = fminf(least, fabsf(y[e / kVec][e % kVec]));
     }
-    *reinterpret_cast<uint2*>(h + it.a) =
-        make_uint2(e4m3x4(a[k][0], a[k][1], a[k][2], a[k][3]), e4m3x4(a[k][4], a[k][5], a[k][6], a[k][7]));
-    *reinterpret_cast<uint2*>(h + it.b) =
-        make_uint2(e4m3x4(b[k][0], b[k][1], b[k][2], b[k][3]), e4m3x4(b[k][4], b[k][5], b[k][6], b[k][7]));
+    if (divide || !(least >= 0x1p-6f)) {
+#pragma unroll
+      for (int e = 0; e < 2 * kVec; ++e)
+        y[e / kVec][e % kVec] = __fdiv_rn(mend ? finite(v[e / kVec][e % kVec]) : v[e / kVec][e % kVec], scale);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      *reinterpret_cast<uint2*>(out + head * p.d + (u ? it.b : it.a)) =
+          make_uint2(e4m3x4(y[u][0], y[u][1], y[u][2], y[u][3]), e4m3x4(y[u][4], y[u][5], y[u][6], y[u][7]));
   }
   if (l == 0) p.scale[dst] = scale;
 }
 
-template <int DT, int G>
+template <int DT, int G, int NI>
 static dsa_status launch_quantise_g(const QuantParams& p, cudaStream_t stream) {
   constexpr int kRows = kQuantThreads / G;
   const size_t smem = static_cast<size_t>(kRows) * (p.r.rot / 2) * sizeof(float2);
   const int64_t grid = (p.T + kRows - 1) / kRows;
-  index_quantise_kernel<DT, G><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
+  index_quantise_kernel<DT, G, NI><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
 template <int DT>
 static dsa_status launch_quantise_t(const QuantParams& p, cudaStream_t stream) {
   const int n = p.H * (p.d / kItem);
-  if (n <= 8) return launch_quantise_g<DT, 8>(p, stream);
-  if (n <= 16) return launch_quantise_g<DT, 16>(p, stream);
-  if (n <= 32) return launch_quantise_g<DT, 32>(p, stream);
-  return launch_quantise_g<DT, kQuantThreads>(p, stream);
+  if (n <= 8) return launch_quantise_g<DT, 8, 1>(p, stream);
+  if (n <= 16) return launch_quantise_g<DT, 16, 1>(p, stream);
+  if (n <= 32) return launch_quantise_g<DT, 32, 1>(p, stream);
+  if (n <= 4 * kQuantThreads) return launch_quantise_g<DT, kQuantThreads, 4>(p, stream);
+  return launch_quantise_g<DT, kQuantThreads, kQuantMaxRow / kItem / kQuantThreads>(p, stream);
 }
 
-dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream) {
+dsa_status launch_quantise(const QuantParams& in, int dtype, cudaStream_t stream) {
+  QuantParams p = in;
+  const uint32_t per_head = p.d / kItem;
+  p.per_head_inv = ((1u << 20) + per_head - 1) / per_head;
   if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16>(p, stream);
   if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16>(p, stream);
   return launch_quantise_t<DSA_DTYPE_F32>(p, stream);

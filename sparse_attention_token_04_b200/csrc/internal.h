@@ -1,6 +1,7 @@
 // Internal launch interface between the C-ABI layer (api.cu) and the kernel files.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -188,6 +189,7 @@ struct QuantParams {
   uint8_t* codes;
   float* scale;
   WsHeader* hdr;
+  uint32_t per_head_inv;        // filled in by launch_quantise
 };
 dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream);
 struct ReadParams {
@@ -263,6 +265,21 @@ bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, u
 // 128-byte swizzle.
 bool encode_tmap_3d_16(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint64_t row_stride,
                        uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_outer);
+
+// Lets a kernel use `bytes` (the same on every call) of dynamic shared memory; asked of the runtime once
+// per device.
+template <auto Kernel>
+inline bool allow_shared(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (done.load() & bit)) return true;
+  if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+    return false;
+  done.fetch_or(bit);
+  return true;
+}
 
 inline dsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 

@@ -695,11 +695,9 @@ static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t str
                    part + static_cast<size_t>(row_tiles) * n_cta * 2 * kLdDv * HT, a.hdr, a.budget_ns};
   const size_t smem = sizeof(LdSmem<HT>) + 1024;
   static_assert(sizeof(LdSmem<HT>) + 1024 <= 227 * 1024, "shared memory");
-  const size_t csmem = (static_cast<size_t>(n_cta) * HT + HT * Lc<HT>::kPitch) * sizeof(float);
-  if (cudaFuncSetAttribute(latent_decode_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess ||
-      cudaFuncSetAttribute(latent_combine_kernel<DT, HT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(csmem)) != cudaSuccess)
+  // (At most one CTA a row tile and SM.)
+  const size_t csmem = (static_cast<size_t>(a.num_sms) * HT + HT * Lc<HT>::kPitch) * sizeof(float);
+  if (!allow_shared<latent_decode_kernel<DT, HT>>(smem) || !allow_shared<latent_combine_kernel<DT, HT>>(csmem))
     return DSA_ERR_CUDA;
   latent_decode_kernel<DT, HT><<<dim3(row_tiles, n_cta), kLdThreads, smem, stream>>>(map, p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;

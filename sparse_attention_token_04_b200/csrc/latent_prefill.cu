@@ -365,9 +365,7 @@ static dsa_status launch_prefill_dt(const LatentPrefillParams& a, cudaStream_t s
                    a.out, a.lse, a.hdr, a.budget_ns};
   const size_t smem = sizeof(LpSmem) + 1024;
   static_assert(sizeof(LpSmem) + 1024 <= 227 * 1024, "shared memory");
-  if (cudaFuncSetAttribute(latent_prefill_kernel<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  if (!allow_shared<latent_prefill_kernel<DT>>(smem)) return DSA_ERR_CUDA;
   const dim3 grid(a.H, (a.max_q + 2 * kLpTile - 1) / (2 * kLpTile), a.B);
   latent_prefill_kernel<DT><<<grid, kLpThreads, smem, stream>>>(mq, mk, mpe, mv, p);
   return cuda_status(cudaGetLastError());

@@ -59,18 +59,27 @@ __device__ __forceinline__ void rotary_pair(float2 cs, float& a, float& b) {
   b = __fmaf_rn(b0, cs.x, __fmul_rn(a0, cs.y));
 }
 
-// Eight consecutive elements as fp32 and back. The pointers are 16-byte aligned.
+// Eight consecutive elements: as they lie in memory, as fp32, and back. The pointers are 16-byte aligned.
+template <int DT>
+struct RawVec {
+  uint4 w[DT == DSA_DTYPE_F32 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ RawVec<DT> load_raw(const typename Elem<DT>::T* p) {
+  RawVec<DT> r;
+  r.w[0] = *reinterpret_cast<const uint4*>(p);
+  if constexpr (DT == DSA_DTYPE_F32) r.w[1] = *reinterpret_cast<const uint4*>(p + 4);
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack_raw(const RawVec<DT>& r, float (&v)[kVec]) {
+  const typename Elem<DT>::T* e = reinterpret_cast<const typename Elem<DT>::T*>(&r);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) v[i] = Elem<DT>::get(e[i]);
+}
 template <int DT>
 __device__ __forceinline__ void load_vec(const typename Elem<DT>::T* p, float (&v)[kVec]) {
-  if constexpr (DT == DSA_DTYPE_F32) {
-    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-  } else {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p);
-    const typename Elem<DT>::T* e = reinterpret_cast<const typename Elem<DT>::T*>(&raw);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = Elem<DT>::get(e[i]);
-  }
+  unpack_raw<DT>(load_raw<DT>(p), v);
 }
 template <int DT>
 __device__ __forceinline__ void store_vec(typename Elem<DT>::T* p, const float (&v)[kVec]) {

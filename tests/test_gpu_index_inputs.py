@@ -146,6 +146,28 @@ def test_quantise_without_rotation_is_exact(dtype, T, H, d):
     assert np.array_equal(e4m3_decode(got), e4m3_decode(c))   # -0 and 0 are the same value
 
 
+def test_quantise_next_to_every_border_between_codes():
+    """fp32 rows whose quotients lie within a few ulps of the middle of two neighbouring codes, for rows of
+    many magnitudes, and all codes' own values: each code is that of the fp32 quotient."""
+    v = O.e4m3_values()
+    mids = np.concatenate([(v[1:] + v[:-1]) / 2, v[:-1]])
+    g = np.random.RandomState(5)
+    rows = []
+    for k in range(60):
+        top = np.float32(448.0 * 2.0 ** g.randint(-100, 100) * (1 + g.rand()))
+        scale = np.float32(top) / np.float32(448.0)
+        x = (mids * np.float64(scale)).astype(np.float32)
+        x = np.maximum(x.view(np.int32) + g.randint(-4, 5, x.shape), 0).astype(np.int32).view(np.float32)
+        x = np.clip(x, 0, top) * g.choice([-1, 1], x.shape).astype(np.float32)
+        rows.append(np.concatenate([x, np.zeros(255 - len(x), np.float32), [top]]))
+    x = np.stack(rows).astype(np.float32)
+    assert x.shape == (60, 256)
+    codes, scale = B.dsa_index_quantise(torch.from_numpy(x).cuda())
+    c, s = O.quantise(x)
+    assert np.array_equal(scale.cpu().numpy(), s)
+    assert np.array_equal(e4m3_decode(codes.cpu().numpy()), e4m3_decode(c))
+
+
 def test_quantise_smallest_and_largest_rows():
     x = torch.zeros(4, 128)
     x[0, 5] = 1e-45
