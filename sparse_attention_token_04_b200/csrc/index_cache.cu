@@ -17,13 +17,6 @@ namespace dsa {
 
 constexpr int kQuantThreads = 128;
 
-// Whether a quotient y of magnitude >= 2^-6 lies within four ulps of a border between two codes (their
-// middle: the mantissa bits behind E4M3's three are 1000...).
-__device__ __forceinline__ bool near_border(float y) {
-  const uint32_t u = __float_as_uint(y);
-  return ((u + 4u) & 0xFFFFFu) - 0x80000u <= 8u;
-}
-
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
@@ -35,28 +28,83 @@ __device__ __forceinline__ float finite(float v) {
   if (fabsf(v) <= FLT_MAX) return v;
   return isnan(v) ? 0.0f : copysignf(FLT_MAX, v);
 }
-// The larger of two non-negative values, NaN if either is.
-__device__ __forceinline__ float max_or_nan(float a, float b) {
+// The largest of three magnitudes, NaN if any is.
+__device__ __forceinline__ float max_or_nan(float a, float b, float c) {
   float m;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
+// The codes of four quotients from products with the reciprocal, taken a little (2^-21) too small (lo)
+// and too large (hi). The rounded reciprocal's product is within 2^-22 of the quotient, so where both
+// give the same codes they are the quotients'; else `differ` is set.
+__device__ __forceinline__ uint32_t e4m3x4_of(const float* v, float lo, float hi, bool& differ) {
+  const uint32_t x = e4m3x4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo);
+  differ |= x != e4m3x4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi);
+  return x;
+}
 
-// G threads of a CTA take one row of up to NI * G items, so a CTA takes 128 / G rows: short rows (up to
-// 32 items) one item a thread, so that one warp holds whole rows and needs no barrier for their maxima,
-// others all 128 threads. The values stay packed as they were loaded (every load of a row is in flight
-// at once, and six CTAs fit an SM) and are rotated twice, for the maximum and for the codes. (As fp32
-// with 256 threads, two CTAs an SM: 301 us for 16384 x 64 x 128 bf16 values, against a floor of 62.)
-template <int DT, int G, int NI>
-__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) index_quantise_kernel(const QuantParams p) {
+// Makes the compiler take the values as new: it would keep the first rotation's results, twice the
+// registers, for the second.
+template <int DT>
+__device__ __forceinline__ void keep_packed(RawVec<DT>& r) {
+#pragma unroll
+  for (uint4& w : r.w) asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w));
+}
+
+// The rare paths, out of line so that they hold no registers of the kernel's: the maximum of a row with
+// values that are not finite, over the others, and an item's codes by division.
+template <int DT, bool INTERLEAVED>
+static __device__ __noinline__ float finite_max(const QuantParams* p, const typename Elem<DT>::T* row, const float2* cs) {
+  const int per_head = p->d / kItem;
+  float top = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < p->H * per_head; ++i) {
+    const Item it = rotary_item(i % per_head, p->r);
+    const typename Elem<DT>::T* h = row + (i / per_head) * p->xs_h;
+    float a[kVec], b[kVec];
+    load_vec<DT>(h + it.a, a);
+    load_vec<DT>(h + it.b, b);
+    if (it.f >= 0) rotary_turn<INTERLEAVED>(cs + it.f, a, b);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaxf(fabsf(finite(a[e])), fabsf(finite(b[e]))));
+  }
+  return top;
+}
+template <int DT, bool INTERLEAVED>
+static __device__ __noinline__ void divided_item(const typename Elem<DT>::T* a, const typename Elem<DT>::T* b,
+                                                 const float2* cs, float scale, uint8_t* out_a, uint8_t* out_b) {
+  float v[2][kVec];
+  load_vec<DT>(a, v[0]);
+  load_vec<DT>(b, v[1]);
+  if (cs) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) v[u][e] = __fdiv_rn(finite(v[u][e]), scale);
+    *reinterpret_cast<uint2*>(u ? out_b : out_a) =
+        make_uint2(e4m3x4(v[u][0], v[u][1], v[u][2], v[u][3]), e4m3x4(v[u][4], v[u][5], v[u][6], v[u][7]));
+  }
+}
+
+// G threads of a CTA take one row, so a CTA takes 128 / G rows: rows of up to 32 items one item a
+// thread (one warp then holds whole rows and needs no barrier for their maxima), others all 128
+// threads. A thread has the same item of every (128 / items of a head)th head, so that it finds its
+// offsets and the eight (cos, sin) that it needs once. The values stay packed as they were loaded (every
+// load of a row is in flight at once, and six CTAs fit an SM) and are rotated twice, for the maximum and
+// for the codes.
+template <int DT, bool INTERLEAVED, int G, int NI>
+__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) index_quantise_kernel(const __grid_constant__ QuantParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kRows = kQuantThreads / G;
-  extern __shared__ float2 cs_all[];
+  extern __shared__ __align__(16) float2 cs_all[];
   __shared__ float warp_max[kQuantThreads / 32];
   const int half = p.r.rot / 2;
   const int g = threadIdx.x / G, l = threadIdx.x % G;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows, t = t0 + g;
-  const int per_head = p.d / kItem, n = p.H * per_head;
+  const int per_head = p.d / kItem, head0 = l / per_head, heads = G / per_head;
+  const Item it = rotary_item(l - head0 * per_head, p.r);
+  // The thread's items: heads head0, head0 + heads, ...
+  const int last = head0 < heads || NI == 1 ? p.H : 0;
   int64_t dst = -1;
   if (t < p.T) {
     dst = p.slots ? p.slots[t] : t;
@@ -65,16 +113,12 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
       dst = -1;
     }
   }
-  // i / per_head for i < 1024 (per_head_inv = ceil(2^20 / per_head)).
-  auto head_of = [&](int i) { return static_cast<int>((static_cast<uint32_t>(i) * p.per_head_inv) >> 20); };
   RawVec<DT> ra[NI], rb[NI];
   const T* row = static_cast<const T*>(p.x) + t * p.xs_t;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int i = l + k * G;
-    if (dst < 0 || i >= n) continue;
-    const int head = head_of(i);
-    const Item it = rotary_item(i - head * per_head, p.r);
+    const int head = head0 + k * heads;
+    if (dst < 0 || head >= last) continue;
     const T* h = row + head * p.xs_h;
     ra[k] = load_raw<DT>(h + it.a);
     rb[k] = load_raw<DT>(h + it.b);
@@ -84,107 +128,104 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
     if (tt < p.T) cs_all[i] = rotary_cos_sin(p.r.positions[tt], p.r.inv_freq[i % half], p.r);
   }
   __syncthreads();
+  float2 cs[kVec];
+  if (it.f >= 0) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) cs[i] = cs_all[g * half + it.f + i];
+  }
+  auto turned = [&](const RawVec<DT>& xa, const RawVec<DT>& xb, float (&a)[kVec], float (&b)[kVec]) {
+    unpack_raw<DT>(xa, a);
+    unpack_raw<DT>(xb, b);
+    if (it.f >= 0) rotary_turn<INTERLEAVED>(cs, a, b);
+  };
   float top = 0.0f;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int i = l + k * G;
-    if (dst < 0 || i >= n) continue;
+    if (dst < 0 || head0 + k * heads >= last) continue;
     float a[kVec], b[kVec];
-    unpack_raw<DT>(ra[k], a);
-    unpack_raw<DT>(rb[k], b);
-    rotary_turn(rotary_item(i - head_of(i) * per_head, p.r), p.r, cs_all + g * half, a, b);
+    turned(ra[k], rb[k], a, b);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) top = max_or_nan(top, max_or_nan(fabsf(a[e]), fabsf(b[e])));
+    for (int e = 0; e < kVec; ++e) top = max_or_nan(top, a[e], b[e]);
   }
 #pragma unroll
   for (int off = (G < 32 ? G : 32) / 2; off > 0; off >>= 1)
-    top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off), 0.0f);
   if constexpr (G > 32) {
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < G / 32; ++w) top = max_or_nan(top, warp_max[w]);
+    for (int w = 0; w < G / 32; ++w) top = max_or_nan(top, warp_max[w], 0.0f);
   }
   if (dst < 0) return;
-  // A row with a value that is not finite: its maximum is not finite either, and is taken over the others.
+  // A row with a value that is not finite: its maximum is not finite either, and is found anew by every
+  // thread from the whole row.
   const bool mend = !(top <= FLT_MAX);
   if (mend) {
     if (l == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_NOT_FINITE);
-    top = 0.0f;
-    for (int i = 0; i < n; ++i) {  // (every thread goes through the whole row: it is a bad one)
-      const int head = head_of(i);
-      const Item it = rotary_item(i - head * per_head, p.r);
-      float a[kVec], b[kVec];
-      load_vec<DT>(row + head * p.xs_h + it.a, a);
-      load_vec<DT>(row + head * p.xs_h + it.b, b);
-      rotary_turn(it, p.r, cs_all + g * half, a, b);
-#pragma unroll 1
-      for (int e = 0; e < kVec; ++e) top = fmaxf(top, fmaxf(fabsf(finite(a[e])), fabsf(finite(b[e]))));
-    }
+    top = finite_max<DT, INTERLEAVED>(&p, row, cs_all + g * half);
   }
   const float scale = top > 0.0f ? fmaxf(__fdiv_rn(top, 448.0f), FLT_MIN) : 1.0f;
-  // The product with the rounded reciprocal is within two ulps of the quotient. It has the quotient's
-  // code unless it is that close to a border between codes or, where the codes' steps no longer scale
-  // with the value, below 2^-6: the item is then divided, a few in a hundred.
-  const float inv = __fdiv_rn(1.0f, scale);
+  const float inv = __fdiv_rn(1.0f, scale), lo = inv * (1.0f - 0x1p-21f), hi = inv * (1.0f + 0x1p-21f);
   uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d);
+  uint32_t again = 0;                           // items to be divided
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int i = l + k * G;
-    if (i >= n) continue;
-    const int head = head_of(i);
-    const Item it = rotary_item(i - head * per_head, p.r);
-    float v[2][kVec], y[2][kVec];
-    unpack_raw<DT>(ra[k], v[0]);
-    unpack_raw<DT>(rb[k], v[1]);
-    rotary_turn(it, p.r, cs_all + g * half, v[0], v[1]);
-    bool divide = mend;
-    float least = INFINITY;
-#pragma unroll
-    for (int e = 0; e < 2 * kVec; ++e) {
-      y[e / kVec][e % kVec] = v[e / kVec][e % kVec] * inv;
-      divide |= near_border(y[e / kVec][e % kVec]);
-      least = fminf(least, fabsf(y[e / kVec][e % kVec]));
-    }
-    if (divide || !(least >= 0x1p-6f)) {
-#pragma unroll
-      for (int e = 0; e < 2 * kVec; ++e)
-        y[e / kVec][e % kVec] = __fdiv_rn(mend ? finite(v[e / kVec][e % kVec]) : v[e / kVec][e % kVec], scale);
-    }
+    const int head = head0 + k * heads;
+    if (head >= last) continue;
+    float v[2][kVec];
+    keep_packed(ra[k]);
+    keep_packed(rb[k]);
+    turned(ra[k], rb[k], v[0], v[1]);
+    bool differ = mend;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
       *reinterpret_cast<uint2*>(out + head * p.d + (u ? it.b : it.a)) =
-          make_uint2(e4m3x4(y[u][0], y[u][1], y[u][2], y[u][3]), e4m3x4(y[u][4], y[u][5], y[u][6], y[u][7]));
+          make_uint2(e4m3x4_of(v[u], lo, hi, differ), e4m3x4_of(v[u] + 4, lo, hi, differ));
+    again |= static_cast<uint32_t>(differ) << k;
+  }
+  // A few items in a thousand, or all of a row that is mended, read again.
+#pragma unroll 1
+  for (int k = 0; again; ++k, again >>= 1) {
+    if (!(again & 1u)) continue;
+    const int head = head0 + k * heads;
+    const T* h = row + head * p.xs_h;
+    divided_item<DT, INTERLEAVED>(h + it.a, h + it.b, it.f >= 0 ? cs_all + g * half + it.f : nullptr, scale,
+                                  out + head * p.d + it.a, out + head * p.d + it.b);
   }
   if (l == 0) p.scale[dst] = scale;
 }
 
-template <int DT, int G, int NI>
+template <int DT, bool INTERLEAVED, int G, int NI>
 static dsa_status launch_quantise_g(const QuantParams& p, cudaStream_t stream) {
   constexpr int kRows = kQuantThreads / G;
   const size_t smem = static_cast<size_t>(kRows) * (p.r.rot / 2) * sizeof(float2);
   const int64_t grid = (p.T + kRows - 1) / kRows;
-  index_quantise_kernel<DT, G, NI><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
+  index_quantise_kernel<DT, INTERLEAVED, G, NI><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
-template <int DT>
+template <int DT, bool INTERLEAVED>
 static dsa_status launch_quantise_t(const QuantParams& p, cudaStream_t stream) {
-  const int n = p.H * (p.d / kItem);
-  if (n <= 8) return launch_quantise_g<DT, 8, 1>(p, stream);
-  if (n <= 16) return launch_quantise_g<DT, 16, 1>(p, stream);
-  if (n <= 32) return launch_quantise_g<DT, 32, 1>(p, stream);
-  if (n <= 4 * kQuantThreads) return launch_quantise_g<DT, kQuantThreads, 4>(p, stream);
-  return launch_quantise_g<DT, kQuantThreads, kQuantMaxRow / kItem / kQuantThreads>(p, stream);
+  const int per_head = p.d / kItem, n = p.H * per_head;
+  if (n <= 8) return launch_quantise_g<DT, INTERLEAVED, 8, 1>(p, stream);
+  if (n <= 16) return launch_quantise_g<DT, INTERLEAVED, 16, 1>(p, stream);
+  if (n <= 32) return launch_quantise_g<DT, INTERLEAVED, 32, 1>(p, stream);
+  if (p.H <= 4 * (kQuantThreads / per_head)) return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 4>(p, stream);
+  return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 8>(p, stream);
 }
 
-dsa_status launch_quantise(const QuantParams& in, int dtype, cudaStream_t stream) {
-  QuantParams p = in;
-  const uint32_t per_head = p.d / kItem;
-  p.per_head_inv = ((1u << 20) + per_head - 1) / per_head;
-  if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16>(p, stream);
-  if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16>(p, stream);
-  return launch_quantise_t<DSA_DTYPE_F32>(p, stream);
+// Rows that a thread can hold: eight items, each of another head (8 * (128 / items of a head) heads).
+bool quantise_row_fits(int H, int d) { return d <= kQuantThreads * kItem && H <= 8 * (kQuantThreads * kItem / d); }
+
+dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream) {
+  if (p.r.interleaved) {
+    if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, true>(p, stream);
+    if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, true>(p, stream);
+    return launch_quantise_t<DSA_DTYPE_F32, true>(p, stream);
+  }
+  if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, false>(p, stream);
+  if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, false>(p, stream);
+  return launch_quantise_t<DSA_DTYPE_F32, false>(p, stream);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -177,7 +177,7 @@ void rotary_frequencies(int rot, double theta, double factor, int original_len, 
 
 // Quantisation of index queries and keys and the paged key cache (index_cache.cu). A row is a
 // token's H x d values; r.rot = 0 quantises without a rotation.
-constexpr int kQuantMaxRow = 16384;
+bool quantise_row_fits(int H, int d);  // whether one CTA's registers hold a row
 struct QuantParams {
   RotaryArgs r;
   const void* x;
@@ -189,7 +189,6 @@ struct QuantParams {
   uint8_t* codes;
   float* scale;
   WsHeader* hdr;
-  uint32_t per_head_inv;        // filled in by launch_quantise
 };
 dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream);
 struct ReadParams {

@@ -11,11 +11,11 @@ namespace dsa {
 
 constexpr int kRotThreads = 256;
 
-template <int DT>
+template <int DT, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs r, const typename Elem<DT>::T* x, int64_t xs_t,
                                                              int64_t xs_h, typename Elem<DT>::T* out, int64_t os_t,
                                                              int64_t os_h, int32_t H, int32_t d, bool in_place) {
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   const int64_t t = blockIdx.x;
   const int per_head = in_place ? r.rot / kItem : d / kItem;  // in place, copied items stay as they are
   const int n = H * per_head;
@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs r, const
       load_vec<DT>(row + head * xs_h + it.a, a);
       load_vec<DT>(row + head * xs_h + it.b, b);
     }
-    rotary_turn(it, r, cs, a, b);
+    if (it.f >= 0) rotary_turn<INTERLEAVED>(cs + it.f, a, b);
     typename Elem<DT>::T* o = out + t * os_t + head * os_h;
     store_vec<DT>(o + it.a, a);
     store_vec<DT>(o + it.b, b);
@@ -50,7 +50,7 @@ template <int DT>
 __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(RotaryArgs r, const typename Elem<DT>::T* x,
                                                                  int64_t xs_t, int64_t xs_h, typename Elem<DT>::T* out,
                                                                  int64_t os_t, int64_t os_h, int32_t H, int32_t d) {
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   const int64_t t = blockIdx.x;
   const int32_t p = r.positions[t];
   const int half = r.rot / 2;
@@ -89,8 +89,10 @@ static dsa_status launch_rotary_t(const RotaryLaunch& a) {
   // Few tokens: a token's items are spread over CTAs until the GPU has one CTA per SM.
   const int64_t fill = (a.num_sms + a.T - 1) / a.T, need = (n + kRotThreads - 1) / kRotThreads;
   const dim3 grid(a.T, static_cast<unsigned>(need < fill ? need : fill));
-  if (wide)
-    rotary_kernel<DT><<<grid, kRotThreads, smem, a.stream>>>(a.r, x, a.xs_t, a.xs_h, out, a.os_t, a.os_h, a.H, a.d, in_place);
+  if (wide && a.r.interleaved)
+    rotary_kernel<DT, true><<<grid, kRotThreads, smem, a.stream>>>(a.r, x, a.xs_t, a.xs_h, out, a.os_t, a.os_h, a.H, a.d, in_place);
+  else if (wide)
+    rotary_kernel<DT, false><<<grid, kRotThreads, smem, a.stream>>>(a.r, x, a.xs_t, a.xs_h, out, a.os_t, a.os_h, a.H, a.d, in_place);
   else
     rotary_any_kernel<DT><<<grid, kRotThreads, smem, a.stream>>>(a.r, x, a.xs_t, a.xs_h, out, a.os_t, a.os_h, a.H, a.d);
   return cuda_status(cudaGetLastError());

@@ -114,19 +114,17 @@ __device__ __forceinline__ Item rotary_item(int j, const RotaryArgs& r) {
   return Item{a, b, -1};
 }
 
-// Turns an item's values; cs: (cos, sin) of the token's frequencies.
-__device__ __forceinline__ void rotary_turn(const Item& it, const RotaryArgs& r, const float2* cs, float (&a)[kVec],
-                                            float (&b)[kVec]) {
-  if (it.f < 0) return;
-  if (r.interleaved) {
+// Turns an item's values; cs: the (cos, sin) of its eight frequencies.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotary_turn(const float2* cs, float (&a)[kVec], float (&b)[kVec]) {
 #pragma unroll
-    for (int i = 0; i < kVec; i += 2) {
-      rotary_pair(cs[it.f + i / 2], a[i], a[i + 1]);
-      rotary_pair(cs[it.f + 4 + i / 2], b[i], b[i + 1]);
+  for (int i = 0; i < kVec; ++i) {
+    if constexpr (INTERLEAVED) {
+      float(&v)[kVec] = i < 4 ? a : b;
+      rotary_pair(cs[i], v[2 * (i & 3)], v[2 * (i & 3) + 1]);
+    } else {
+      rotary_pair(cs[i], a[i], b[i]);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) rotary_pair(cs[it.f + i], a[i], b[i]);
   }
 }
 
