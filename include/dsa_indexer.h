@@ -343,8 +343,8 @@ DSA_API dsa_status dsa_rotary_frequencies(int32_t rot, double theta, double fact
  *   x        [T][H][d] (dsa_index_quantise) or [T][d] bf16, f16 or f32 (dtype), element strides
  *            x_stride_t, x_stride_h and 1; 16-byte aligned, strides multiples of 8 elements
  *   slots    [T] i64
- * T >= 0; d <= 2048 and rot multiples of 16, rot_offset a multiple of 8, H <= 8 * floor(2048 / d) (128
- * heads of 128 dims; else DSA_ERR_UNSUPPORTED).
+ * T >= 0; d <= 2048 and rot multiples of 16, rot_offset a multiple of 8, H * d <= 16384 (else
+ * DSA_ERR_UNSUPPORTED).
  *
  * dsa_index_cache_read copies positions starts[b] .. starts[b] + n_b - 1 of every request b (n_b =
  * cu_rows[b + 1] - cu_rows[b]; starts = NULL: from 0) from the paged cache to rows cu_rows[b] .. of

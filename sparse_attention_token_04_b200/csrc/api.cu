@@ -84,7 +84,7 @@ dsa_status check_quantise(const void* x, int64_t xs_t, int64_t xs_h, int64_t T, 
     if (rot % 16 || rot_offset % 8 || rot > DSA_MAX_ROTARY) return DSA_ERR_UNSUPPORTED;
     *r = RotaryArgs{positions, inv_freq, rot, rot_offset, interleaved != 0, 0, mscale};
   }
-  if (d % 16 || !quantise_row_fits(H, d)) return DSA_ERR_UNSUPPORTED;
+  if (d % 16 || d > kQuantMaxDim || static_cast<int64_t>(H) * d > kQuantMaxRow) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
 
@@ -336,7 +336,7 @@ DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_s
   if (values_dtype < DSA_DTYPE_BF16 || values_dtype > DSA_DTYPE_F32) return DSA_ERR_INVALID;
   if (!aligned(k_cache, 16) || !aligned(out_codes, 16) || !aligned(out_values, 16)) return DSA_ERR_INVALID;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < DSA_WS_HEADER_BYTES) return DSA_ERR_INVALID;
-  if (d % 16 || d > 2048) return DSA_ERR_UNSUPPORTED;
+  if (d % 16 || d > kQuantMaxDim) return DSA_ERR_UNSUPPORTED;
   if (total == 0 || (!out_codes && !out_scale && !out_values)) return DSA_OK;
   const ReadParams p{k_cache, k_scale_cache, n_blocks, block_size, d, block_table, max_blocks, starts,
                      cu_rows, B, total, out_codes, out_scale, out_values, static_cast<WsHeader*>(workspace)};

@@ -8,6 +8,7 @@
 // one launch (a decode step): each value is read once and kept in registers between the row's
 // maximum and its codes.
 #include <cfloat>
+#include <type_traits>
 
 #include <cuda_fp8.h>
 
@@ -86,14 +87,35 @@ static __device__ __noinline__ void divided_item(const typename Elem<DT>::T* a, 
   }
 }
 
+// The absolute maximum of an item that is not rotated, NaN if any value is: 16-bit values are compared
+// packed.
+template <int DT>
+__device__ __forceinline__ float raw_max(float top, const RawVec<DT>& a, const RawVec<DT>& b) {
+  if constexpr (DT == DSA_DTYPE_F32) {
+    const float *x = reinterpret_cast<const float*>(&a), *y = reinterpret_cast<const float*>(&b);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) top = max_or_nan(top, x[e], y[e]);
+    return top;
+  } else {
+    using T2 = std::conditional_t<DT == DSA_DTYPE_BF16, __nv_bfloat162, __half2>;
+    const T2 *x = reinterpret_cast<const T2*>(&a), *y = reinterpret_cast<const T2*>(&b);
+    T2 m = __habs2(x[0]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = __hmax2_nan(m, __hmax2_nan(__habs2(x[e]), __habs2(y[e])));
+    return max_or_nan(top, Elem<DT>::get(m.x), Elem<DT>::get(m.y));
+  }
+}
+
 // G threads of a CTA take one row, so a CTA takes 128 / G rows: rows of up to 32 items one item a
 // thread (one warp then holds whole rows and needs no barrier for their maxima), others all 128
-// threads. A thread has the same item of every (128 / items of a head)th head, so that it finds its
-// offsets and the eight (cos, sin) that it needs once. The values stay packed as they were loaded (every
-// load of a row is in flight at once, and six CTAs fit an SM) and are rotated twice, for the maximum and
-// for the codes.
+// threads in up to NI passes, first over the heads' rotated items and then over the copied ones, so that
+// a pass is either for every thread. In every pass a thread has the same item of another head: it finds
+// its offsets and the eight (cos, sin) that it needs once. The values stay packed as they were loaded
+// (every load of a row is in flight at once, and six CTAs fit an SM); rotated ones are rotated twice,
+// for the maximum and for the codes.
 template <int DT, bool INTERLEAVED, int G, int NI>
-__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) index_quantise_kernel(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1)
+    index_quantise_kernel(const __grid_constant__ QuantParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kRows = kQuantThreads / G;
   extern __shared__ __align__(16) float2 cs_all[];
@@ -101,10 +123,29 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
   const int half = p.r.rot / 2;
   const int g = threadIdx.x / G, l = threadIdx.x % G;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows, t = t0 + g;
-  const int per_head = p.d / kItem, head0 = l / per_head, heads = G / per_head;
-  const Item it = rotary_item(l - head0 * per_head, p.r);
-  // The thread's items: heads head0, head0 + heads, ...
-  const int last = head0 < heads || NI == 1 ? p.H : 0;
+  const int n_rot = p.r.rot / kItem, n_copy = p.d / kItem - n_rot;
+  // The thread's rotated items: item j_rot of heads h_rot, h_rot + per_rot, ... below end_rot (passes 0 to
+  // passes_rot - 1); its copied ones alike. With one item a thread they are told apart by its number.
+  int per_rot = 1, per_copy = 1, passes_rot = 0, h_rot = 0, h_copy = 0, j_rot = 0, j_copy = 0, end_rot = 0, end_copy = 0;
+  if (n_rot) {
+    per_rot = NI == 1 ? p.H : G / n_rot;
+    passes_rot = NI == 1 ? (l < p.H * n_rot) : (p.H + per_rot - 1) / per_rot;
+    h_rot = l / n_rot;
+    j_rot = l - h_rot * n_rot;
+    end_rot = h_rot < per_rot ? p.H : 0;
+  }
+  if (n_copy) {
+    const int lc = NI == 1 ? l - p.H * n_rot : l;
+    per_copy = NI == 1 ? p.H : G / n_copy;
+    h_copy = lc / n_copy;
+    j_copy = lc - h_copy * n_copy;
+    end_copy = lc >= 0 && h_copy < per_copy ? p.H : 0;
+  }
+  const Item ir = rotary_item(j_rot, p.r), ic = rotary_item(n_rot + j_copy, p.r);
+  auto head_of = [&](int k) {                   // of pass k, -1: none for this thread
+    const int head = k < passes_rot ? h_rot + k * per_rot : h_copy + (k - passes_rot) * per_copy;
+    return head < (k < passes_rot ? end_rot : end_copy) ? head : -1;
+  };
   int64_t dst = -1;
   if (t < p.T) {
     dst = p.slots ? p.slots[t] : t;
@@ -117,11 +158,11 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
   const T* row = static_cast<const T*>(p.x) + t * p.xs_t;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int head = head0 + k * heads;
-    if (dst < 0 || head >= last) continue;
+    const int head = head_of(k);
+    if (dst < 0 || head < 0) continue;
     const T* h = row + head * p.xs_h;
-    ra[k] = load_raw<DT>(h + it.a);
-    rb[k] = load_raw<DT>(h + it.b);
+    ra[k] = load_raw<DT>(h + (k < passes_rot ? ir.a : ic.a));
+    rb[k] = load_raw<DT>(h + (k < passes_rot ? ir.b : ic.b));
   }
   for (int i = threadIdx.x; i < kRows * half; i += kQuantThreads) {
     const int64_t tt = t0 + i / half;
@@ -129,23 +170,24 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
   }
   __syncthreads();
   float2 cs[kVec];
-  if (it.f >= 0) {
+  if (n_rot) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) cs[i] = cs_all[g * half + it.f + i];
+    for (int i = 0; i < kVec; ++i) cs[i] = cs_all[g * half + ir.f + i];
   }
-  auto turned = [&](const RawVec<DT>& xa, const RawVec<DT>& xb, float (&a)[kVec], float (&b)[kVec]) {
-    unpack_raw<DT>(xa, a);
-    unpack_raw<DT>(xb, b);
-    if (it.f >= 0) rotary_turn<INTERLEAVED>(cs, a, b);
-  };
   float top = 0.0f;
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    if (dst < 0 || head0 + k * heads >= last) continue;
-    float a[kVec], b[kVec];
-    turned(ra[k], rb[k], a, b);
+    if (dst < 0 || head_of(k) < 0) continue;
+    if (k < passes_rot) {
+      float a[kVec], b[kVec];
+      unpack_raw<DT>(ra[k], a);
+      unpack_raw<DT>(rb[k], b);
+      rotary_turn<INTERLEAVED>(cs, a, b);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) top = max_or_nan(top, a[e], b[e]);
+      for (int e = 0; e < kVec; ++e) top = max_or_nan(top, a[e], b[e]);
+    } else {
+      top = raw_max<DT>(top, ra[k], rb[k]);
+    }
   }
 #pragma unroll
   for (int off = (G < 32 ? G : 32) / 2; off > 0; off >>= 1)
@@ -170,16 +212,19 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
   uint32_t again = 0;                           // items to be divided
 #pragma unroll
   for (int k = 0; k < NI; ++k) {
-    const int head = head0 + k * heads;
-    if (head >= last) continue;
+    const int head = head_of(k);
+    if (head < 0) continue;
     float v[2][kVec];
     keep_packed(ra[k]);
     keep_packed(rb[k]);
-    turned(ra[k], rb[k], v[0], v[1]);
+    unpack_raw<DT>(ra[k], v[0]);
+    unpack_raw<DT>(rb[k], v[1]);
+    if (k < passes_rot) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
     bool differ = mend;
+    uint8_t* o = out + head * p.d;
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<uint2*>(out + head * p.d + (u ? it.b : it.a)) =
+      *reinterpret_cast<uint2*>(o + (k < passes_rot ? (u ? ir.b : ir.a) : (u ? ic.b : ic.a))) =
           make_uint2(e4m3x4_of(v[u], lo, hi, differ), e4m3x4_of(v[u] + 4, lo, hi, differ));
     again |= static_cast<uint32_t>(differ) << k;
   }
@@ -187,7 +232,8 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1) inde
 #pragma unroll 1
   for (int k = 0; again; ++k, again >>= 1) {
     if (!(again & 1u)) continue;
-    const int head = head0 + k * heads;
+    const int head = head_of(k);
+    const Item& it = k < passes_rot ? ir : ic;
     const T* h = row + head * p.xs_h;
     divided_item<DT, INTERLEAVED>(h + it.a, h + it.b, it.f >= 0 ? cs_all + g * half + it.f : nullptr, scale,
                                   out + head * p.d + it.a, out + head * p.d + it.b);
@@ -204,18 +250,25 @@ static dsa_status launch_quantise_g(const QuantParams& p, cudaStream_t stream) {
   return cuda_status(cudaGetLastError());
 }
 
+// Passes over a row of H heads by all threads; at most 18 with 1024 items (a pass takes more than half of
+// the threads).
+static int quantise_passes(const QuantParams& p) {
+  const int n_rot = p.r.rot / kItem, n_copy = p.d / kItem - n_rot;
+  int passes = 0;
+  for (const int n : {n_rot, n_copy})
+    if (n) passes += (p.H + kQuantThreads / n - 1) / (kQuantThreads / n);
+  return passes;
+}
+
 template <int DT, bool INTERLEAVED>
 static dsa_status launch_quantise_t(const QuantParams& p, cudaStream_t stream) {
-  const int per_head = p.d / kItem, n = p.H * per_head;
+  const int n = p.H * (p.d / kItem);
   if (n <= 8) return launch_quantise_g<DT, INTERLEAVED, 8, 1>(p, stream);
   if (n <= 16) return launch_quantise_g<DT, INTERLEAVED, 16, 1>(p, stream);
   if (n <= 32) return launch_quantise_g<DT, INTERLEAVED, 32, 1>(p, stream);
-  if (p.H <= 4 * (kQuantThreads / per_head)) return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 4>(p, stream);
-  return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 8>(p, stream);
+  if (quantise_passes(p) <= 4) return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 4>(p, stream);
+  return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 18>(p, stream);
 }
-
-// Rows that a thread can hold: eight items, each of another head (8 * (128 / items of a head) heads).
-bool quantise_row_fits(int H, int d) { return d <= kQuantThreads * kItem && H <= 8 * (kQuantThreads * kItem / d); }
 
 dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream) {
   if (p.r.interleaved) {

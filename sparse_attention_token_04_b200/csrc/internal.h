@@ -177,7 +177,7 @@ void rotary_frequencies(int rot, double theta, double factor, int original_len, 
 
 // Quantisation of index queries and keys and the paged key cache (index_cache.cu). A row is a
 // token's H x d values; r.rot = 0 quantises without a rotation.
-bool quantise_row_fits(int H, int d);  // whether one CTA's registers hold a row
+constexpr int kQuantMaxRow = 16384, kQuantMaxDim = 2048;
 struct QuantParams {
   RotaryArgs r;
   const void* x;

@@ -195,7 +195,8 @@ def test_quantise_not_finite_is_reported_and_yields_valid_codes():
 
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,H,d,rot,offset", [(50, 64, 128, 64, 0), (3, 8, 64, 32, 8), (70, 1, 128, 64, 64),
-                                              (1, 1, 64, 64, 0)])
+                                              (1, 1, 64, 64, 0), (2, 128, 128, 32, 16), (3, 7, 1040, 1024, 8),
+                                              (2, 64, 128, 128, 0), (2, 9, 144, 48, 40), (2, 4, 48, 16, 24)])
 def test_quantise_with_rotation(T, H, d, rot, offset, interleaved):
     x, pos = _randn((T, H, d), 7, torch.bfloat16), _positions(T, 3)
     f, m = B.dsa_rotary_frequencies(rot, factor=40.0)
