@@ -35,13 +35,16 @@ __device__ __forceinline__ float max_or_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
-// The codes of four quotients from products with the reciprocal, taken a little (2^-21) too small (lo)
-// and too large (hi). The rounded reciprocal's product is within 2^-22 of the quotient, so where both
-// give the same codes they are the quotients'; else `differ` is set.
-__device__ __forceinline__ uint32_t e4m3x4_of(const float* v, float lo, float hi, bool& differ) {
-  const uint32_t x = e4m3x4(v[0] * lo, v[1] * lo, v[2] * lo, v[3] * lo);
-  differ |= x != e4m3x4(v[0] * hi, v[1] * hi, v[2] * hi, v[3] * hi);
-  return x;
+// v / scale for inv = 1 / scale, both rounded to nearest: the product's remainder is exact, and with it
+// the product is corrected to the rounded quotient (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990), as long as nothing underflows, which kLeastScale sees to.
+// Checked against divisions next to every border between two codes. (Products that were checked against
+// the borders and divided where close cost more: bf16 values meet borders exactly often enough that
+// every third warp divided.)
+constexpr float kLeastScale = 0x1p-90f;
+__device__ __forceinline__ float quotient(float v, float scale, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-q, scale, v), inv, q);
 }
 
 // Makes the compiler take the values as new: it would keep the first rotation's results, twice the
@@ -53,7 +56,7 @@ __device__ __forceinline__ void keep_packed(RawVec<DT>& r) {
 }
 
 // The rare paths, out of line so that they hold no registers of the kernel's: the maximum of a row with
-// values that are not finite, over the others, and an item's codes by division.
+// values that are not finite, over the others, and an item's codes by division (of such rows and of very small ones).
 template <int DT, bool INTERLEAVED>
 static __device__ __noinline__ float finite_max(const QuantParams* p, const typename Elem<DT>::T* row, const float2* cs) {
   const int per_head = p->d / kItem;
@@ -111,10 +114,10 @@ __device__ __forceinline__ float raw_max(float top, const RawVec<DT>& a, const R
 // threads in up to NI passes, first over the heads' rotated items and then over the copied ones, so that
 // a pass is either for every thread. In every pass a thread has the same item of another head: it finds
 // its offsets and the eight (cos, sin) that it needs once. The values stay packed as they were loaded
-// (every load of a row is in flight at once, and six CTAs fit an SM); rotated ones are rotated twice,
+// (every load of a row is in flight at once, and five CTAs fit an SM); rotated ones are rotated twice,
 // for the maximum and for the codes.
 template <int DT, bool INTERLEAVED, int G, int NI>
-__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1)
+__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 5 : 1)
     index_quantise_kernel(const __grid_constant__ QuantParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kRows = kQuantThreads / G;
@@ -207,36 +210,38 @@ __global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 6 : 1)
     top = finite_max<DT, INTERLEAVED>(&p, row, cs_all + g * half);
   }
   const float scale = top > 0.0f ? fmaxf(__fdiv_rn(top, 448.0f), FLT_MIN) : 1.0f;
-  const float inv = __fdiv_rn(1.0f, scale), lo = inv * (1.0f - 0x1p-21f), hi = inv * (1.0f + 0x1p-21f);
+  const float inv = __fdiv_rn(1.0f, scale);
   uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d);
-  uint32_t again = 0;                           // items to be divided
-#pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int head = head_of(k);
-    if (head < 0) continue;
-    float v[2][kVec];
-    keep_packed(ra[k]);
-    keep_packed(rb[k]);
-    unpack_raw<DT>(ra[k], v[0]);
-    unpack_raw<DT>(rb[k], v[1]);
-    if (k < passes_rot) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
-    bool differ = mend;
-    uint8_t* o = out + head * p.d;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-      *reinterpret_cast<uint2*>(o + (k < passes_rot ? (u ? ir.b : ir.a) : (u ? ic.b : ic.a))) =
-          make_uint2(e4m3x4_of(v[u], lo, hi, differ), e4m3x4_of(v[u] + 4, lo, hi, differ));
-    again |= static_cast<uint32_t>(differ) << k;
-  }
-  // A few items in a thousand, or all of a row that is mended, read again.
+  if (mend || scale < kLeastScale) {
 #pragma unroll 1
-  for (int k = 0; again; ++k, again >>= 1) {
-    if (!(again & 1u)) continue;
-    const int head = head_of(k);
-    const Item& it = k < passes_rot ? ir : ic;
-    const T* h = row + head * p.xs_h;
-    divided_item<DT, INTERLEAVED>(h + it.a, h + it.b, it.f >= 0 ? cs_all + g * half + it.f : nullptr, scale,
-                                  out + head * p.d + it.a, out + head * p.d + it.b);
+    for (int k = 0; k < NI; ++k) {
+      const int head = head_of(k);
+      if (head < 0) continue;
+      const Item& it = k < passes_rot ? ir : ic;
+      const T* h = row + head * p.xs_h;
+      divided_item<DT, INTERLEAVED>(h + it.a, h + it.b, it.f >= 0 ? cs_all + g * half + it.f : nullptr, scale,
+                                    out + head * p.d + it.a, out + head * p.d + it.b);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int head = head_of(k);
+      if (head < 0) continue;
+      float v[2][kVec];
+      keep_packed(ra[k]);
+      keep_packed(rb[k]);
+      unpack_raw<DT>(ra[k], v[0]);
+      unpack_raw<DT>(rb[k], v[1]);
+      if (k < passes_rot) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
+      uint8_t* o = out + head * p.d;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) v[u][e] = quotient(v[u][e], scale, inv);
+        *reinterpret_cast<uint2*>(o + (k < passes_rot ? (u ? ir.b : ir.a) : (u ? ic.b : ic.a))) =
+            make_uint2(e4m3x4(v[u][0], v[u][1], v[u][2], v[u][3]), e4m3x4(v[u][4], v[u][5], v[u][6], v[u][7]));
+      }
+    }
   }
   if (l == 0) p.scale[dst] = scale;
 }
