@@ -20,6 +20,7 @@
 // Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
 // take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,7 +41,7 @@ struct LpSmem {
   uint8_t k[kLpKStages][3][kLpBlock];
   uint8_t v[2][kLpBlock];
   uint64_t q_full[2], k_full[kLpKStages], k_empty[kLpKStages], v_full, v_empty;
-  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem;
   int abort;
 };
@@ -99,7 +100,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.q_full[i], 1);
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_ready[i], 4);
+      mbar_init(&sm.p_ready[i][0], 4);
+      mbar_init(&sm.p_ready[i][1], 4);
       mbar_init(&sm.o_done[i], 1);
     }
     for (int i = 0; i < kLpKStages; ++i) {
@@ -185,13 +187,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         tc_commit(&sm.s_full[w]);
       };
-      auto pv = [&](int w, int j) {
-        const uint32_t vb = smem_u32(sm.v[0]);
+      // The PV of 64 keys: P comes in two halves.
+      auto pv = [&](int w, int j, int half) {
+        tc_fence_after();
+        const uint64_t dv = make_smem_desc_mn(smem_u32(sm.v[0]), kLpBlock, 1024);
 #pragma unroll
-        for (int kk = 0; kk < kLpTile / 16; ++kk)
-          tc_mma_16_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, make_smem_desc_mn(vb + kk * 2048, kLpBlock, 1024),
-                       idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-        tc_commit(&sm.o_done[w]);
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_16_ts(tmem + 256 + w * 128, tmem + w * 128 + (half * 4 + kk) * 8, dv + ((half * 4 + kk) * 2048 >> 4),
+                       idesc_pv, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
       };
       bool ok = mbar_wait_call(&sm.k_full[0], 0, ctl, DETAIL_WAIT_KFULL);
       for (int w = 0; w < 2 && ok; ++w) {
@@ -207,10 +210,13 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         for (int w = 0; w < 2 && ok; ++w) {
           if (j < nt[w]) {
             ok = mbar_wait_call(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL) &&
-                 mbar_wait_call(&sm.p_ready[w], j & 1, ctl, DETAIL_WAIT_SCORES);
+                 mbar_wait_call(&sm.p_ready[w][0], j & 1, ctl, DETAIL_WAIT_SCORES);
             if (!ok) break;
-            tc_fence_after();
-            pv(w, j);
+            pv(w, j, 0);
+            ok = mbar_wait_call(&sm.p_ready[w][1], j & 1, ctl, DETAIL_WAIT_SCORES);
+            if (!ok) break;
+            pv(w, j, 1);
+            tc_commit(&sm.o_done[w]);
             if (w == last) tc_commit(&sm.v_empty);
           }
           if (j + 1 < nt[w]) {
@@ -242,24 +248,37 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       if (!ok) break;
       tc_fence_after();
       uint32_t s[4][32];
+      tmem_ld_32x32b_x32(tS, s[0]);
+      tmem_ld_32x32b_x32(tS + 32, s[1]);
+      tmem_wait_ld_regs(s[0]);
+      tmem_wait_ld_regs(s[1]);
+      tmem_ld_32x32b_x32(tS + 64, s[2]);
+      tmem_ld_32x32b_x32(tS + 96, s[3]);
+      const bool masked = (j + 1) * kLpTile > n_warp;
+      const int left = n_row - j * kLpTile;  // visible keys of this tile
+      auto mask = [&](int c) {
+        if (!masked) return;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tS + c * 32, s[c]);
+        for (int e = 0; e < 32; ++e)
+          if (c * 32 + e >= left) s[c][e] = 0xFF800000u;  // -inf
+      };
+      float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+      auto row_max = [&](int c) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_wait_ld_regs(s[c]);
-      if ((j + 1) * kLpTile > n_warp) {
-        const int left = n_row - j * kLpTile;  // visible keys of this tile
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= left) s[c][e] = 0xFF800000u;  // -inf
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[c][e]));
-      const float mn = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), m);
+        for (int e = 0; e < 32; e += 2)
+          mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(s[c][e])), __uint_as_float(s[c][e + 1]));
+      };
+      mask(0);
+      mask(1);
+      row_max(0);
+      row_max(1);
+      tmem_wait_ld_regs(s[2]);
+      tmem_wait_ld_regs(s[3]);
+      mask(2);
+      mask(3);
+      row_max(2);
+      row_max(3);
+      const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       if (j == 0) {
         m = mn;
       } else if (__any_sync(0xFFFFFFFFu, (mn - m) * p.scale_log2 > kLpLazy)) {
@@ -281,37 +300,45 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         }
         tmem_wait_st();
       }
-      const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < 4; c += 2) {
-        uint32_t packed[32];
-#pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float p0 = exp2_fast(fmaf(__uint_as_float(s[c + (e >> 5)][e & 31]), p.scale_log2, base));
-          const float p1 = exp2_fast(fmaf(__uint_as_float(s[c + (e >> 5)][(e & 31) + 1]), p.scale_log2, base));
-          sum[e & 2] += p0;
-          sum[(e & 2) + 1] += p1;
-          packed[e >> 1] = pack_16<DT>(p0, p1);
-        }
-        tmem_st_32x32b_x32(tS + c * 16, packed);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if ((j + 1) * kLpTile > nk) {
         // Rows of V behind the request's last key belong to others: zero weights must meet zeros.
         ok = mbar_wait_warp(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL);
-        if (ok && row >= nk - j * kLpTile)
-#pragma unroll
+        if (!ok) break;
+        if (row >= nk - j * kLpTile)
+#pragma unroll 1
           for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sm.v[c] + row * 128 + u * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
-        if (!ok) break;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_ready[w]);
+      const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
+      const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), base2 = make_float2(base, base);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      // The numerators of 64 keys, rounded into P; of an unmasked tile every fourth pair by polynomial.
+      auto numerators = [&](int half, auto poly) {
+        uint32_t packed[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const uint32_t* v = &s[half * 2 + (e >> 5)][e & 31];
+          const float2 x = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale2, base2);
+          const float2 q = decltype(poly)::value && (e & 6) == 6 ? exp2_poly(x) : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], q);
+          packed[e >> 1] = pack_16<DT>(q.x, q.y);
+        }
+        tmem_st_32x32b_x32(tS + half * 32, packed);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[w][half]);
+      };
+      if (masked) {
+        numerators(0, std::false_type{});
+        numerators(1, std::false_type{});
+      } else {
+        numerators(0, std::true_type{});
+        numerators(1, std::true_type{});
+      }
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
     tc_fence_after();
