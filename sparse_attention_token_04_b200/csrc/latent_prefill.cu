@@ -20,7 +20,6 @@
 // Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
 // take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
 #include <cmath>
-#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -314,14 +313,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
       const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), base2 = make_float2(base, base);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      // The numerators of 64 keys, rounded into P; of an unmasked tile every fourth pair by polynomial.
-      auto numerators = [&](int half, auto poly) {
+      // The numerators of 64 keys, rounded into P.
+      auto numerators = [&](int half) {
         uint32_t packed[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           const uint32_t* v = &s[half * 2 + (e >> 5)][e & 31];
           const float2 x = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale2, base2);
-          const float2 q = decltype(poly)::value && (e & 6) == 6 ? exp2_poly(x) : make_float2(exp2_fast(x.x), exp2_fast(x.y));
+          const float2 q = make_float2(exp2_fast(x.x), exp2_fast(x.y));
           sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], q);
           packed[e >> 1] = pack_16<DT>(q.x, q.y);
         }
@@ -331,13 +330,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[w][half]);
       };
-      if (masked) {
-        numerators(0, std::false_type{});
-        numerators(1, std::false_type{});
-      } else {
-        numerators(0, std::true_type{});
-        numerators(1, std::true_type{});
-      }
+      numerators(0);
+      numerators(1);
       l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
