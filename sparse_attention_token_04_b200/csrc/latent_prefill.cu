@@ -311,18 +311,18 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         fence_proxy_async_smem();
       }
       const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
-      const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), base2 = make_float2(base, base);
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       // The numerators of 64 keys, rounded into P.
       auto numerators = [&](int half) {
         uint32_t packed[32];
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
           const uint32_t* v = &s[half * 2 + (e >> 5)][e & 31];
-          const float2 x = fma2(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), scale2, base2);
-          const float2 q = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], q);
-          packed[e >> 1] = pack_16<DT>(q.x, q.y);
+          const float p0 = exp2_fast(fmaf(__uint_as_float(v[0]), p.scale_log2, base));
+          const float p1 = exp2_fast(fmaf(__uint_as_float(v[1]), p.scale_log2, base));
+          sum[e & 2] += p0;
+          sum[(e & 2) + 1] += p1;
+          packed[e >> 1] = pack_16<DT>(p0, p1);
         }
         tmem_st_32x32b_x32(tS + half * 32, packed);
         tmem_wait_st();
@@ -331,8 +331,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         if (lane == 0) mbar_arrive(&sm.p_ready[w][half]);
       };
       numerators(0);
+      // (Nothing of the second half is computed before the first is on its way.)
+#pragma unroll
+      for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[2][e]), "+r"(s[3][e]));
       numerators(1);
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
     tc_fence_after();
