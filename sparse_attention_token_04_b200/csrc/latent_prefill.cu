@@ -9,13 +9,14 @@
 //   warps 0-3, 4-7  softmax of query tile 0, 1: running maximum m and sum l of the row, O rescaled
 //                   in TMEM only when m has grown by more than 2^kLazy (so that the accumulator is
 //                   touched a few times per row, not every tile); at the end O / l and lse;
-//   warp 8          TMA: the query tiles once, K tiles two deep, V tiles one deep (a V tile's
-//                   successor is needed two S products after it is released);
+//   warp 8          TMA: the query tiles once, K in blocks of 16 KB (three a tile) through a ring of
+//                   four, V tiles two deep;
 //   warp 9          one thread issues every MMA, in the order PV(0, j), QK(0, j+1), PV(1, j),
 //                   QK(1, j+1). QK(w, j+1) overwrites the columns that PV(w, j) reads P from: both go
 //                   down the one tensor pipe in issue order.
-// Shared memory: 96 KB of Q, 96 KB of K, 32 KB of V, all [128 rows][64 dims] blocks with the 128-byte
-// swizzle. TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and 384-511.
+// Shared memory: 96 KB of Q, 64 KB of K, 64 KB of V, all [128 rows][64 dims] blocks with the 128-byte
+// swizzle. (With K two tiles and V one tile deep instead, a V tile came 1000 cycles late every time; in
+// one ring of blocks for both, V's two blocks are not neighbours and PV takes twice the MMAs.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and 384-511.
 //
 // Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
 // take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
@@ -32,14 +33,14 @@ namespace dsa {
 constexpr int kLpTile = 128;                 // query rows of a tile, keys of a tile
 constexpr int kLpThreads = 320;
 constexpr int kLpBlock = kLpTile * 128;      // 16 KB: 128 rows x 64 dims
-constexpr int kLpKStages = 2;
+constexpr int kLpKRing = 4;                  // blocks of the K ring (a tile has three)
 constexpr float kLpLazy = 6.0f;              // log2 growth of a row's maximum that is left unscaled
 
 struct LpSmem {
   uint8_t q[2][3][kLpBlock];
-  uint8_t k[kLpKStages][3][kLpBlock];
-  uint8_t v[2][kLpBlock];
-  uint64_t q_full[2], k_full[kLpKStages], k_empty[kLpKStages], v_full, v_empty;
+  uint8_t k[kLpKRing][kLpBlock];
+  uint8_t v[2][2][kLpBlock];
+  uint64_t q_full[2], k_full[kLpKRing], k_free[kLpKRing], v_full[2], v_free[2];
   uint64_t s_full[2], p_ready[2][2], o_done[2], drain;
   uint32_t tmem;
   int abort;
@@ -102,13 +103,13 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       mbar_init(&sm.p_ready[i][0], 4);
       mbar_init(&sm.p_ready[i][1], 4);
       mbar_init(&sm.o_done[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_free[i], 1);
     }
-    for (int i = 0; i < kLpKStages; ++i) {
+    for (int i = 0; i < kLpKRing; ++i) {
       mbar_init(&sm.k_full[i], 1);
-      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.k_free[i], 1);
     }
-    mbar_init(&sm.v_full, 1);
-    mbar_init(&sm.v_empty, 1);
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.abort = 0;
@@ -130,43 +131,45 @@ __global__ void __launch_bounds__(kLpThreads, 1)
         for (int c = 0; c < 3; ++c)
           tma_load_3d(sm.q[w][c], &map_q, c * 64, h, q0 + i0 + w * kLpTile, &sm.q_full[w]);
       };
-      auto load_k = [&](int j) {
-        const int st = j % kLpKStages;
-        if (!mbar_wait_call(&sm.k_empty[st], ((j / kLpKStages) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
-        mbar_arrive_expect_tx(&sm.k_full[st], 3 * kLpBlock);
-        for (int c = 0; c < 2; ++c) tma_load_3d(sm.k[st][c], &map_k, c * 64, h, k0 + j * kLpTile, &sm.k_full[st]);
-        tma_load_3d(sm.k[st][2], &map_pe, 0, 0, k0 + j * kLpTile, &sm.k_full[st]);
+      // K blocks g = 3 j + c in their order; V of tile j behind K's first block of the tile (of tile 0:
+      // behind its last), which is the order in which their places come free.
+      int g = 0, nv = 0;
+      bool ok = true;
+      auto load_v = [&]() {
+        const int st = nv & 1;
+        if (!mbar_wait_call(&sm.v_free[st], ((nv >> 1) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
+        mbar_arrive_expect_tx(&sm.v_full[st], 2 * kLpBlock);
+        for (int c = 0; c < 2; ++c) tma_load_3d(sm.v[st][c], &map_v, c * 64, h, k0 + nv * kLpTile, &sm.v_full[st]);
+        ++nv;
         return true;
       };
-      auto load_v = [&](int j) {
-        if (!mbar_wait_call(&sm.v_empty, (j & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY)) return false;
-        mbar_arrive_expect_tx(&sm.v_full, 2 * kLpBlock);
-        for (int c = 0; c < 2; ++c) tma_load_3d(sm.v[c], &map_v, c * 64, h, k0 + j * kLpTile, &sm.v_full);
-        return true;
-      };
-      int nk_issued = 0, nv_issued = 0;
-      if (n_tiles > 0) {
-        if (nt[0] > 0) load_q(0);
-        if (load_k(0)) ++nk_issued;
-        if (nt[1] > 0) load_q(1);
-        for (int j = 0; j < n_tiles; ++j) {
-          // K tile j + 1 is released (by the S products of tile j - 1) before V tile j is (by PV j - 1)
-          if (j + 1 < n_tiles) {
-            if (!load_k(j + 1)) break;
-            ++nk_issued;
-          }
-          if (!load_v(j)) break;
-          ++nv_issued;
+      if (nt[0] > 0) load_q(0);
+#pragma unroll 1
+      for (; g < 3 * n_tiles; ++g) {
+        const int j = g / 3, c = g - 3 * j, slot = g % kLpKRing, key = k0 + j * kLpTile;
+        ok = mbar_wait_call(&sm.k_free[slot], ((g / kLpKRing) & 1) ^ 1, ctl, DETAIL_WAIT_KEMPTY);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&sm.k_full[slot], kLpBlock);
+        if (c < 2) tma_load_3d(sm.k[slot], &map_k, c * 64, h, key, &sm.k_full[slot]);
+        else tma_load_3d(sm.k[slot], &map_pe, 0, 0, key, &sm.k_full[slot]);
+        if (g == 2) {
+          if (nt[1] > 0) load_q(1);
+          ok = load_v();
+        } else if (g > 2 && c == 0) {
+          ok = load_v();
         }
-        // Let every copy land before the CTA exits (bounded).
-        for (int w = 0; w < 2; ++w)
-          if (nt[w] > 0) mbar_drain_call(&sm.q_full[w], 0, p.budget_ns);
-        for (int st = 0; st < kLpKStages; ++st) {
-          const int n = (nk_issued - st + kLpKStages - 1) / kLpKStages;
-          if (n > 0) mbar_drain_call(&sm.k_full[st], (n - 1) & 1, p.budget_ns);
+        if (!ok) {
+          ++g;
+          break;
         }
-        if (nv_issued > 0) mbar_drain_call(&sm.v_full, (nv_issued - 1) & 1, p.budget_ns);
       }
+      // Let every copy land before the CTA exits (bounded).
+      for (int w = 0; w < 2; ++w)
+        if (nt[w] > 0 && (w == 0 || g > 2)) mbar_drain_call(&sm.q_full[w], 0, p.budget_ns);
+#pragma unroll 1
+      for (int i = max(0, g - kLpKRing); i < g; ++i) mbar_drain_call(&sm.k_full[i % kLpKRing], (i / kLpKRing) & 1, p.budget_ns);
+#pragma unroll 1
+      for (int i = max(0, nv - 2); i < nv; ++i) mbar_drain_call(&sm.v_full[i & 1], (i >> 1) & 1, p.budget_ns);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -174,58 +177,57 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       constexpr uint32_t bf16 = DT == DSA_DTYPE_BF16 ? 1u : 0u;
       constexpr uint32_t idesc_qk = make_idesc_16(bf16, kLpTile, kLpTile);
       constexpr uint32_t idesc_pv = make_idesc_16(bf16, kLpTile, 128) | kIdescBMnMajor;
-      auto qk = [&](int w, int j) {
-        const int st = j % kLpKStages;
+      const uint64_t dk = make_smem_desc(smem_u32(sm.k[0]), 128);
+      const uint64_t dv = make_smem_desc_mn(smem_u32(sm.v[0][0]), kLpBlock, 1024);
+      // `first`, `last`: whether this query tile is the first or the last to use the key tile.
+      auto qk = [&](int w, int j, bool first, bool last) {
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          const uint64_t da = make_smem_desc(smem_u32(sm.q[w][c]), 128);
-          const uint64_t db = make_smem_desc(smem_u32(sm.k[st][c]), 128);
+          const int g = 3 * j + c, slot = g % kLpKRing;
+          if (first) {
+            if (!mbar_wait_call(&sm.k_full[slot], (g / kLpKRing) & 1, ctl, DETAIL_WAIT_KFULL)) return false;
+            tc_fence_after();
+          }
+          const uint64_t da = make_smem_desc(smem_u32(sm.q[w][c]), 128), db = dk + slot * (kLpBlock >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_bf16(tmem + w * 128, da + 2ull * kk, db + 2ull * kk, idesc_qk, (c > 0 || kk > 0) ? 1u : 0u);
+          if (last) tc_commit(&sm.k_free[slot]);
         }
         tc_commit(&sm.s_full[w]);
+        return true;
       };
       // The PV of 64 keys: P comes in two halves.
       auto pv = [&](int w, int j, int half) {
+        if (!mbar_wait_call(&sm.p_ready[w][half], j & 1, ctl, DETAIL_WAIT_SCORES)) return false;
         tc_fence_after();
-        const uint64_t dv = make_smem_desc_mn(smem_u32(sm.v[0]), kLpBlock, 1024);
+        const uint64_t db = dv + (j & 1) * (2 * kLpBlock >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_16_ts(tmem + 256 + w * 128, tmem + w * 128 + (half * 4 + kk) * 8, dv + ((half * 4 + kk) * 2048 >> 4),
-                       idesc_pv, (j > 0 || half > 0 || kk > 0) ? 1u : 0u);
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+          tc_mma_16_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, db + (kk * 2048 >> 4), idesc_pv,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+        return true;
       };
-      bool ok = mbar_wait_call(&sm.k_full[0], 0, ctl, DETAIL_WAIT_KFULL);
+      const bool both = nt[0] > 0 && nt[1] > 0;
+      bool ok = true;
       for (int w = 0; w < 2 && ok; ++w) {
         if (nt[w] == 0) continue;
-        ok = mbar_wait_call(&sm.q_full[w], 0, ctl, DETAIL_WAIT_QFULL);
-        if (!ok) break;
-        tc_fence_after();
-        qk(w, 0);
+        ok = mbar_wait_call(&sm.q_full[w], 0, ctl, DETAIL_WAIT_QFULL) && qk(w, 0, w == 0 || !both, w == 1 || !both);
       }
-      if (ok) tc_commit(&sm.k_empty[0]);
+#pragma unroll 1
       for (int j = 0; j < n_tiles && ok; ++j) {
-        const int last = j < nt[1] ? 1 : 0;  // the query tile whose PV is the last of this key tile
-        for (int w = 0; w < 2 && ok; ++w) {
-          if (j < nt[w]) {
-            ok = mbar_wait_call(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL) &&
-                 mbar_wait_call(&sm.p_ready[w][0], j & 1, ctl, DETAIL_WAIT_SCORES);
+        ok = mbar_wait_call(&sm.v_full[j & 1], (j >> 1) & 1, ctl, DETAIL_WAIT_KFULL);
+        const bool two = j < nt[0] && j < nt[1], two_next = j + 1 < nt[0] && j + 1 < nt[1];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (ok && j < nt[w]) {
+            ok = pv(w, j, 0) && pv(w, j, 1);
             if (!ok) break;
-            pv(w, j, 0);
-            ok = mbar_wait_call(&sm.p_ready[w][1], j & 1, ctl, DETAIL_WAIT_SCORES);
-            if (!ok) break;
-            pv(w, j, 1);
             tc_commit(&sm.o_done[w]);
-            if (w == last) tc_commit(&sm.v_empty);
+            if (w == 1 || !two) tc_commit(&sm.v_free[j & 1]);
           }
-          if (j + 1 < nt[w]) {
-            ok = mbar_wait_call(&sm.k_full[(j + 1) % kLpKStages], ((j + 1) / kLpKStages) & 1, ctl, DETAIL_WAIT_KFULL);
-            if (!ok) break;
-            tc_fence_after();
-            qk(w, j + 1);
-          }
+          if (ok && j + 1 < nt[w]) ok = qk(w, j + 1, w == 0 || !two_next, w == 1 || !two_next);
         }
-        if (ok && j + 1 < n_tiles) tc_commit(&sm.k_empty[(j + 1) % kLpKStages]);
       }
       tc_commit(&sm.drain);
       mbar_drain_call(&sm.drain, 0, p.budget_ns);
@@ -301,13 +303,14 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       }
       if ((j + 1) * kLpTile > nk) {
         // Rows of V behind the request's last key belong to others: zero weights must meet zeros.
-        ok = mbar_wait_warp(&sm.v_full, j & 1, ctl, DETAIL_WAIT_KFULL);
+        ok = mbar_wait_warp(&sm.v_full[j & 1], (j >> 1) & 1, ctl, DETAIL_WAIT_KFULL);
         if (!ok) break;
         if (row >= nk - j * kLpTile)
 #pragma unroll 1
           for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) *reinterpret_cast<uint4*>(sm.v[c] + row * 128 + u * 16) = make_uint4(0, 0, 0, 0);
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(sm.v[j & 1][c] + row * 128 + u * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
