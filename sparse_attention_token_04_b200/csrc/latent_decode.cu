@@ -14,11 +14,11 @@
 // products: as K (dims contiguous, K-major) and as V^T (the same bytes, M-major), so every latent is
 // fetched once. O^T has the dims on TMEM lanes and the rows on columns: 4 * HT columns, which is what
 // leaves room beside it (512 dims of 64 rows in 32 bits are half of TMEM).
-//   warps 0-3, 12-15  softmax, the two groups taking the tiles in turn (a thread a row);
-//   warps 4-7  the queries of each segment into shared memory; O^T rescaled (a thread a dim) only when
-//              some row's maximum has grown by more than 2^kLdLazy; the segment's outputs;
-//   warp 8     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
-//   warp 9     one thread issues the QK products, up to four tiles ahead of the softmax;
+//   warps 0-3  the queries of each segment into shared memory; softmax (thread = row, warps 0 and 1
+//              at most); O^T rescaled (thread = dim) only when some row's maximum has grown by more
+//              than 2^kLdLazy; the segment's outputs;
+//   warp 4     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
+//   warp 9     one thread issues the QK products, up to three tiles ahead of the softmax;
 //   warp 10    one thread issues the PV products. (With both in one thread the tensor core idled while
 //              that thread looked at its barriers.)
 // Bound by HBM for up to 64 rows a request (1152 B a key); with 128 rows the products (278528 FLOP a
@@ -37,12 +37,11 @@ namespace dsa {
 constexpr int kLdDqk = 576, kLdDv = 512;
 constexpr int kLdKeys = 32;                     // keys of a tile
 constexpr int kLdChunks = kLdDqk / 64;          // 9
-constexpr int kLdScores = 4;                    // S buffers
+constexpr int kLdScores = 3;                    // S buffers: two QK products ahead of the PV
 constexpr int kLdSlotBytes = kLdKeys * 128;     // 4 KB: one chunk
 constexpr int kLdTileBytes = kLdChunks * kLdSlotBytes;
-constexpr int kLdThreads = 512;
+constexpr int kLdThreads = 352;
 constexpr int kLdLead = 4;                      // rescale factors of this many tiles are kept
-static_assert(kLdScores == kLdLead, "m_ready serves both");
 constexpr float kLdLazy = 6.0f;
 
 template <int HT>
@@ -51,10 +50,8 @@ struct LdSmem {
   uint8_t q[kLdChunks][HT * 128];               // the MMA reads 64 rows from each: into what follows
   uint8_t p[HT * 128];                          // P of two tiles side by side
   uint8_t ring[kStages][kLdTileBytes];
-  float fac[kLdLead][HT];
-  float m_ref[HT];                              // what the rows' numerators are taken against
-  float l_part[2][HT];                          // a segment's sums by softmax group; then [0]: 1 / l
-  uint8_t grow[kLdLead][4];                         // whether a softmax warp's factors are to be applied
+  float fac[kLdLead][HT], inv[HT];
+  int grow[kLdLead][4];                         // whether a softmax warp's factors are to be applied
   uint64_t full[kStages], empty[kStages];       // empty: the tile's PV is done
   uint64_t q_full, s_full[kLdScores], m_ready[kLdLead], p_ready[2], seg_ready, seg_done, drain[2];
   uint32_t tmem;
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     for (int i = 0; i < kLdScores; ++i) mbar_init(&sm.s_full[i], 1);
     for (int i = 0; i < kLdLead; ++i) mbar_init(&sm.m_ready[i], kSoft);
     for (int i = 0; i < 2; ++i) mbar_init(&sm.p_ready[i], kSoft + 4);
-    mbar_init(&sm.seg_ready, 2 * kSoft);
+    mbar_init(&sm.seg_ready, kSoft);
     mbar_init(&sm.seg_done, 4);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
@@ -322,22 +319,16 @@ __global__ void __launch_bounds__(kLdThreads, 1)
       mbar_drain_call(&sm.drain[1], 0, p.budget_ns);
     }
     __syncwarp();
-  } else if (warp < 4 || warp >= 12) {
-    // Softmax: two groups of warps take the tiles in turn. Only the rows' reference m_ref goes from one
-    // tile to the next; each group sums its own tiles' numerators. S of a 64-row MMA has rows 16 w ..
-    // 16 w + 15 on the first 16 TMEM lanes of quarter w: the other half of the warp idles along.
-    const int group = warp >= 12, quarter = warp & 3;
-    if (quarter < kSoft && total > 0) {
-      const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-      const int row = quarter * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
+  } else if (warp < 4) {
+    // Softmax. S of a 64-row MMA has rows 16 w .. 16 w + 15 on the first 16 TMEM lanes of warp w's
+    // quarter: the other half of the warp idles along.
+    if (warp < kSoft && total > 0) {
+      const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+      const int row = warp * 16 + (lane & 15), r = ht * HT + row;  // row of the tile, of the request
       const bool mine = lane < 16;
-      volatile float* m_ref = &sm.m_ref[row];
-      // The tile's reference is there (and so is its S read, and its rescale factors).
-      auto m_ready = [&](int i) {
-        return mbar_wait_warp(&sm.m_ready[i % kLdLead], (i / kLdLead) & 1, ctl, DETAIL_WAIT_SCORES);
-      };
-      int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0;
-      bool ok = true;
+      int b = sm.b0, t = sm.tile0, left = total, done = 0, seg = 0, s_buf = 0, s_ph = 0;
+      bool ok = true, have = false;             // have: s holds the tile's scores already
+      uint32_t s[32], s_next[32];
       while (left > 0 && ok) {
         const int n = ld_len(p, b), nt = (n + kLdKeys - 1) / kLdKeys, te = min(nt, t + left), t_first = t;
         if (te <= t) {                          // a request without keys
@@ -346,58 +337,56 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         }
         left -= te - t;
         const int sees = r < R ? max(0, n - p.q_len + 1 + r / p.Hq) : n;
-        float m = -INFINITY, l = 0.0f;          // the reference that l was summed against
-        auto against = [&](float m_new) {
-          if (m_new != m) l *= exp2_fast((m - m_new) * p.scale_log2);
-          m = m_new;
-        };
+        float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
         for (; t < te; ++t, ++done) {
-          if ((done & 1) != group) continue;
-          uint32_t s[32];
-          ok = mbar_wait_warp(&sm.s_full[done % kLdScores], (done / kLdScores) & 1, ctl, DETAIL_WAIT_ACCFULL);
-          if (!ok) break;
-          tc_fence_after();
-          tmem_ld_32x32b_x32(tmem + (done % kLdScores) * kLdKeys + lanes, s);
-          tmem_wait_ld_regs(s);
+          if (!have) {
+            ok = mbar_wait_warp(&sm.s_full[s_buf], s_ph, ctl, DETAIL_WAIT_ACCFULL);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s);
+            tmem_wait_ld_regs(s);
+          }
+          if (++s_buf == kLdScores) s_buf = 0, s_ph ^= 1;
           const int seen = sees - t * kLdKeys;  // visible keys of this tile
           if (__any_sync(0xFFFFFFFFu, seen < kLdKeys)) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (e >= seen) s[e] = 0xFF800000u;  // -inf
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4] = {m, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mx[(e >> 1) & 3] = fmaxf(fmaxf(mx[(e >> 1) & 3], __uint_as_float(s[e])), __uint_as_float(s[e + 1]));
-          float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          // Rows whose maximum passes the reference by more than 2^kLdLazy take it as the new one and have
-          // what was summed so far scaled down; a segment's first tile sets the references. (-inf - -inf is
-          // NaN and compares false.)
-          bool grow = false;
-          float f = 1.0f;
-          if (t == t_first) {                   // (m_ref and l_part are read for the results of a segment)
-            if (seg > 0) ok = mbar_wait_warp(&sm.seg_done, (seg - 1) & 1, ctl, DETAIL_WAIT_ACCEMPTY);
-            if (!ok) break;
-          } else {
-            ok = m_ready(done - 1);
-            if (!ok) break;
-            const float m_old = *m_ref;
-            grow = mine && (m_new - m_old) * p.scale_log2 > kLdLazy;
-            if (grow) f = exp2_fast((m_old - m_new) * p.scale_log2);
-            else m_new = m_old;
+          for (int e = 0; e < 32; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+          const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // Rows whose maximum has grown by more than 2^kLdLazy have what they summed so far scaled down;
+          // a segment's first tile has nothing yet. (-inf - -inf is NaN and compares false.)
+          bool grow = mine && (mn - m) * p.scale_log2 > kLdLazy;
+          if (t == t_first) {
+            m = mn;
+            grow = false;
           }
           const bool any = __any_sync(0xFFFFFFFFu, grow);
-          if (mine) {
-            if (grow || t == t_first) *m_ref = m_new;
-            if (any) sm.fac[done % kLdLead][row] = f;
+          if (any && mine) {
+            const float f = grow ? exp2_fast((m - mn) * p.scale_log2) : 1.0f;
+            if (grow) m = mn;
+            l *= f;
+            sm.fac[done % kLdLead][row] = f;
           }
-          if (lane == 0) sm.grow[done % kLdLead][quarter] = any;
+          if (lane == 0) sm.grow[done % kLdLead][warp] = any;
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.m_ready[done % kLdLead]);
-          against(m_new);
-          if (done >= 2) ok = pv_done(done - 2);  // the group's half of P's buffer is free
-          if (!ok) break;
+          // The next tile's scores, where they are there already; they arrive behind the exponentials.
+          have = done + 1 < total;
+          if (have) {
+            bool there = false;
+            if (lane == 0) there = mbar_test(&sm.s_full[s_buf], s_ph);
+            have = __shfl_sync(0xFFFFFFFFu, there, 0);
+          }
+          if (have) {
+            tc_fence_after();
+            tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s_next);
+          }
+          if (done >= 2) ok = pv_done(done - 2);  // P's half of the buffer is free
           if (mine) {
             const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -420,15 +409,28 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
+          if (have) {
+            tmem_wait_ld_regs(s_next);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[e] = s_next[e];
+          }
+          if (!ok) break;
         }
         if (!ok) break;
-        // The group's sums against the segment's last reference.
-        if (((done - 1) & 1) != group) {
-          ok = m_ready(done - 1);
-          if (!ok) break;
-          against(*m_ref);
+        // The segment's sums, once the results of the one before are out.
+        if (seg > 0) ok = mbar_wait_warp(&sm.seg_done, (seg - 1) & 1, ctl, DETAIL_WAIT_ACCEMPTY);
+        if (mine) {
+          if (t_first == 0 && te == nt) {
+            sm.inv[row] = l > 0.0f ? 1.0f / l : 0.0f;
+            if (p.lse && r < R)
+              p.lse[static_cast<int64_t>(b) * R + r] =
+                  l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+          } else {
+            float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
+            ml[row] = m;
+            ml[HT + row] = l;
+          }
         }
-        if (mine) sm.l_part[group][row] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.seg_ready);
         ++seg;
@@ -437,8 +439,6 @@ __global__ void __launch_bounds__(kLdThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 11) {
-    // no role
   } else if (total > 0) {
     // Queries, O^T's scaling and the results (warps 4-7; TMEM quarter warp - 4).
     const int quarter = warp - 4, ctid = tid - 128;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         // The tile's scores are complete and read, its rescale factors written.
         ok = mbar_wait_warp(&sm.m_ready[done % kLdLead], (done / kLdLead) & 1, ctl, DETAIL_WAIT_SCORES);
         if (!ok) break;
-        const uint8_t* grow = sm.grow[done % kLdLead];
+        const int* grow = sm.grow[done % kLdLead];
         bool any = false;
 #pragma unroll
         for (int w = 0; w < kSoft; ++w) any |= grow[w] != 0;
@@ -525,20 +525,6 @@ __global__ void __launch_bounds__(kLdThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const bool whole = t_first == 0 && te == nt;
-      if (ctid < HT) {
-        const float m = sm.m_ref[ctid], l = sm.l_part[0][ctid] + sm.l_part[1][ctid];
-        if (whole) {
-          sm.l_part[0][ctid] = l > 0.0f ? 1.0f / l : 0.0f;
-          if (p.lse && ht * HT + ctid < R)
-            p.lse[static_cast<int64_t>(b) * R + ht * HT + ctid] =
-                l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
-        } else {
-          float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
-          ml[ctid] = m;
-          ml[HT + ctid] = l;
-        }
-      }
-      named_bar(1, 128);
       float* part = p.part + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * kLdDv * HT;
 #pragma unroll 1
       for (int c = 0; c < 4 * HT; c += 32) {    // 16 columns at a time, two loads in flight
@@ -554,7 +540,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             uint16_t* out = p.out + (static_cast<int64_t>(b) * R + ht * HT + h0) * kLdDv + dim;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float f = sm.l_part[0][h0 + e];
+              const float f = sm.inv[h0 + e];
               if (ht * HT + h0 + e < R)
                 out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[k][e]) * f) : static_cast<uint16_t>(0);
             }
