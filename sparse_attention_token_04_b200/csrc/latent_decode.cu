@@ -615,6 +615,13 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     // The request's first CTA holds its beginning (slot 1), every other one begins inside it (slot 0).
     const int64_t slot0 = (static_cast<int64_t>(ht) * n_cta + c0) * 2;
     auto slot = [&](int c) { return slot0 + 2 * c + (c == 0 ? 1 : 0); };
+    // The thread's vector of the first eight splits is on its way while the weights are formed.
+    const int dim = tid % kDims, h = tid / kDims * 4;
+    const float* src = p.part + (static_cast<int64_t>(h / 4) * kLdDv + d0 + dim) * 4;
+    auto load = [&](int c) { return __ldcs(reinterpret_cast<const float4*>(src + slot(c) * kLdDv * HT)); };
+    float4 o[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = c < ns ? load(c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     {
       const int row = tid / kPer, c_first = tid % kPer;
       float M = -INFINITY, L = 0.0f;
@@ -641,17 +648,21 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     }
     __syncthreads();
     {
-      const int dim = tid % kDims, h = tid / kDims * 4;
-      const float* src = p.part + (static_cast<int64_t>(h / 4) * kLdDv + d0 + dim) * 4;
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-      for (int c = 0; c < ns; ++c) {
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(src + slot(c) * kLdDv * HT));
-        const float4 w = *reinterpret_cast<const float4*>(wt + c * HT + h);
-        acc.x += w.x * o.x;
-        acc.y += w.y * o.y;
-        acc.z += w.z * o.z;
-        acc.w += w.w * o.w;
+#pragma unroll 1
+      for (int c0 = 0; c0 < ns; c0 += 8) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c0 + c >= ns) break;
+          const float4 w = *reinterpret_cast<const float4*>(wt + (c0 + c) * HT + h);
+          acc.x += w.x * o[c].x;
+          acc.y += w.y * o[c].y;
+          acc.z += w.z * o[c].z;
+          acc.w += w.w * o[c].w;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c0 + 8 + c < ns) o[c] = load(c0 + 8 + c);
       }
       tile[(h + 0) * kPitch + dim] = acc.x;
       tile[(h + 1) * kPitch + dim] = acc.y;
