@@ -522,9 +522,16 @@ def _rows(t, name: str, dtypes, shape) -> None:
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _st(t, i: int) -> int:
-    """Stride of dimension i in elements; that of a dimension of one entry says nothing and is taken as 8."""
-    return t.stride(i) if t.shape[i] > 1 else 8
+def _strides(t):
+    """Strides in elements; that of a dimension of one entry says nothing and is taken as 8."""
+    st = t.stride()
+    return tuple(8 if n == 1 else k for n, k in zip(t.shape, st)) if 1 in t.shape else st
+
+
+def _fits(t, name: str, dtype, shape) -> None:
+    """As _need with a shape; the usual case in one expression."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _need(t, name, dtype, shape)
 
 
 def _addr(t):
@@ -574,11 +581,12 @@ def _rotation(T: int, d: int, positions, inv_freq):
         if inv_freq is not None:
             raise ValueError("inv_freq without positions")
         return 0
-    _need(positions, "positions", torch.int32, (T,))
-    _need(inv_freq, "inv_freq", torch.float32)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have shape (rot // 2,)")
-    return 2 * int(inv_freq.shape[0])
+    _fits(positions, "positions", torch.int32, (T,))
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a tensor of shape (rot // 2,)")
+    half = inv_freq.shape[0]
+    _fits(inv_freq, "inv_freq", torch.float32, (half,))
+    return 2 * half
 
 
 def dsa_rotary_frequencies(rot: int, theta: float = 10000.0, factor: float = 1.0, original_len: int = 4096,
@@ -600,20 +608,21 @@ def dsa_rotary(x, positions, inv_freq, interleaved: bool = False, rot_offset: in
     positions * inv_freq. out may be x; inverse turns back (the gradient of the rotation)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a tensor of shape (T, H, d)")
-    T, H, d = (int(n) for n in x.shape)
-    _rows(x, "x", _DTYPES, (T, H, d))
+    T, H, d = x.shape
+    _rows(x, "x", _DTYPES, x.shape)
     rot = _rotation(T, d, positions, inv_freq)
     if rot == 0:
         raise ValueError("positions and inv_freq are needed")
     s, held = _enter(stream, x, positions, inv_freq, out)
     try:
         if out is None:
-            out = torch.empty(T, H, d, dtype=x.dtype, device=x.device)
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         else:
-            _rows(out, "out", (x.dtype,), (T, H, d))
-        _check(lib().dsa_rotary(_addr(x), _st(x, 0), _st(x, 1), _addr(positions), _addr(inv_freq), T, H, d, rot,
-                                int(rot_offset), int(interleaved), int(inverse), float(mscale), _DTYPES[x.dtype],
-                                _addr(out), _st(out, 0), _st(out, 1), s), "dsa_rotary")
+            _rows(out, "out", (x.dtype,), x.shape)
+        xs, os_ = _strides(x), _strides(out)
+        _check(lib().dsa_rotary(x.data_ptr(), xs[0], xs[1], positions.data_ptr(), inv_freq.data_ptr(), T, H, d, rot,
+                                int(rot_offset), int(interleaved), int(inverse), mscale, _DTYPES[x.dtype],
+                                out.data_ptr(), os_[0], os_[1], s), "dsa_rotary")
     finally:
         _leave(held)
     return out
@@ -625,8 +634,8 @@ def dsa_index_quantise(x, positions=None, inv_freq=None, interleaved: bool = Fal
     positions are given -> (codes u8 of x's shape, scale[T] f32)."""
     if not isinstance(x, torch.Tensor) or x.dim() not in (2, 3):
         raise ValueError("x must be a tensor of shape (T, H, d) or (T, d)")
-    T, d = int(x.shape[0]), int(x.shape[-1])
-    H = int(x.shape[1]) if x.dim() == 3 else 1
+    T, d = x.shape[0], x.shape[-1]
+    H = x.shape[1] if x.dim() == 3 else 1
     _rows(x, "x", _DTYPES, x.shape)
     rot = _rotation(T, d, positions, inv_freq)
     s, held = _enter(stream, x, positions, inv_freq, codes, scale, workspace)
@@ -634,16 +643,17 @@ def dsa_index_quantise(x, positions=None, inv_freq=None, interleaved: bool = Fal
         if codes is None:
             codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
         else:
-            _need(codes, "codes", torch.uint8, x.shape)
+            _fits(codes, "codes", torch.uint8, x.shape)
         if scale is None:
             scale = torch.empty(T, dtype=torch.float32, device=x.device)
         else:
-            _need(scale, "scale", torch.float32, (T,))
+            _fits(scale, "scale", torch.float32, (T,))
         ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s)
-        _check(lib().dsa_index_quantise(_addr(x), _st(x, 0), _st(x, 1) if x.dim() == 3 else 8, T, H, d,
-                                        _DTYPES[x.dtype], _addr(positions), _addr(inv_freq), rot, int(rot_offset),
-                                        int(interleaved), float(mscale), _addr(codes), _addr(scale), _addr(ws),
-                                        ws.numel(), s), "dsa_index_quantise")
+        xs = _strides(x)
+        _check(lib().dsa_index_quantise(x.data_ptr(), xs[0], xs[1] if x.dim() == 3 else 8, T, H, d, _DTYPES[x.dtype],
+                                        _addr(positions), _addr(inv_freq), rot, int(rot_offset), int(interleaved),
+                                        mscale, codes.data_ptr(), scale.data_ptr(), ws.data_ptr(), ws.numel(), s),
+               "dsa_index_quantise")
     finally:
         _leave(held)
     return codes, scale
@@ -656,20 +666,20 @@ def dsa_index_cache_write(x, slots, k_cache, k_scale_cache, positions=None, inv_
     written)."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a tensor of shape (T, d)")
-    T, d = (int(n) for n in x.shape)
-    _rows(x, "x", _DTYPES, (T, d))
-    n_blocks, block_size = int(k_cache.shape[0]), int(k_cache.shape[1])
-    _need(slots, "slots", torch.int64, (T,))
-    _need(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
-    _need(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
+    T, d = x.shape
+    _rows(x, "x", _DTYPES, x.shape)
+    n_blocks, block_size = k_cache.shape[0], k_cache.shape[1]
+    _fits(slots, "slots", torch.int64, (T,))
+    _fits(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
+    _fits(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
     rot = _rotation(T, d, positions, inv_freq)
     s, held = _enter(stream, x, slots, k_cache, k_scale_cache, positions, inv_freq, workspace)
     try:
         ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s)
-        _check(lib().dsa_index_cache_write(_addr(x), _st(x, 0), T, d, _DTYPES[x.dtype], _addr(slots), _addr(positions),
-                                           _addr(inv_freq), rot, int(rot_offset), int(interleaved), float(mscale),
-                                           _addr(k_cache), _addr(k_scale_cache), n_blocks, block_size, _addr(ws),
-                                           ws.numel(), s), "dsa_index_cache_write")
+        _check(lib().dsa_index_cache_write(x.data_ptr(), _strides(x)[0], T, d, _DTYPES[x.dtype], slots.data_ptr(),
+                                           _addr(positions), _addr(inv_freq), rot, int(rot_offset), int(interleaved),
+                                           mscale, k_cache.data_ptr(), k_scale_cache.data_ptr(), n_blocks, block_size,
+                                           ws.data_ptr(), ws.numel(), s), "dsa_index_cache_write")
     finally:
         _leave(held)
 def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: int, starts=None,
@@ -678,15 +688,15 @@ def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: in
     """Reads request ranges of the paged key cache: rows cu_rows[b] .. cu_rows[b + 1] of the outputs are
     positions starts[b] .. (0 .. without starts) of request b -> (codes[total][d] u8, scale[total] f32,
     values[total][d] of the type `values`), the first two None without want_codes, the last without values."""
-    n_blocks, block_size, d = (int(n) for n in k_cache.shape)
-    B = int(block_table.shape[0])
+    n_blocks, block_size, d = k_cache.shape
+    B, max_blocks = block_table.shape
     total = int(total)
-    _need(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
-    _need(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
-    _need(block_table, "block_table", torch.int32, (B, int(block_table.shape[1])))
-    _need(cu_rows, "cu_rows", torch.int32, (B + 1,))
+    _fits(k_cache, "k_cache", torch.uint8, (n_blocks, block_size, d))
+    _fits(k_scale_cache, "k_scale_cache", torch.float32, (n_blocks, block_size))
+    _fits(block_table, "block_table", torch.int32, (B, max_blocks))
+    _fits(cu_rows, "cu_rows", torch.int32, (B + 1,))
     if starts is not None:
-        _need(starts, "starts", torch.int32, (B,))
+        _fits(starts, "starts", torch.int32, (B,))
     if out_values is not None and values is None:
         values = out_values.dtype
     if values is not None and values not in _DTYPES:
@@ -702,16 +712,16 @@ def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: in
         if values is not None and out_values is None:
             out_values = torch.empty(total, d, dtype=values, device=dev)
         if out_codes is not None:
-            _need(out_codes, "out_codes", torch.uint8, (total, d))
+            _fits(out_codes, "out_codes", torch.uint8, (total, d))
         if out_scale is not None:
-            _need(out_scale, "out_scale", torch.float32, (total,))
+            _fits(out_scale, "out_scale", torch.float32, (total,))
         if out_values is not None:
-            _need(out_values, "out_values", values, (total, d))
+            _fits(out_values, "out_values", values, (total, d))
         ws = _workspace(DSA_WS_HEADER_BYTES, dev, workspace, s)
-        _check(lib().dsa_index_cache_read(_addr(k_cache), _addr(k_scale_cache), n_blocks, block_size, d,
-                                          _addr(block_table), int(block_table.shape[1]), _addr(starts), _addr(cu_rows),
-                                          B, total, _addr(out_codes), _addr(out_scale), _addr(out_values),
-                                          _DTYPES.get(values, DSA_DTYPE_F32), _addr(ws), ws.numel(), s),
+        _check(lib().dsa_index_cache_read(k_cache.data_ptr(), k_scale_cache.data_ptr(), n_blocks, block_size, d,
+                                          block_table.data_ptr(), max_blocks, _addr(starts), cu_rows.data_ptr(), B,
+                                          total, _addr(out_codes), _addr(out_scale), _addr(out_values),
+                                          _DTYPES.get(values, DSA_DTYPE_F32), ws.data_ptr(), ws.numel(), s),
                "dsa_index_cache_read")
     finally:
         _leave(held)
@@ -731,15 +741,15 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor of shape (B, q_len, Hq, 576) or (B, Hq, 576)")
     q4 = q if q.dim() == 4 else q[:, None]
-    B, q_len, Hq, dqk = (int(n) for n in q4.shape)
+    B, q_len, Hq, dqk = q4.shape
     _rows(q, "q", _HALF, q.shape)
     if B > 1 and q_len > 1 and q4.stride(0) != q_len * q4.stride(1):
         raise ValueError("q's tokens must be evenly spaced over its requests")
-    q_stride_t = _st(q4, 1) if q_len > 1 else _st(q4, 0)
-    n_rows, dv = int(latent.shape[0]), 512
-    _need(latent, "latent", q.dtype, (n_rows, dqk))
-    _need(block_table, "block_table", torch.int32, (B, int(block_table.shape[1])))
-    _need(seq_lens, "seq_lens", torch.int32, (B,))
+    qs = _strides(q4)
+    n_rows, max_blocks, dv = latent.shape[0], block_table.shape[-1], 512
+    _fits(latent, "latent", q.dtype, (n_rows, dqk))
+    _fits(block_table, "block_table", torch.int32, (B, max_blocks))
+    _fits(seq_lens, "seq_lens", torch.int32, (B,))
     if block_size < 1 or n_rows % block_size:
         raise ValueError("latent rows must be whole blocks")
     s, held = _enter(stream, q, latent, block_table, seq_lens, out, lse, workspace)
@@ -747,16 +757,16 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
         if out is None:
             out = torch.empty(q.shape[:-1] + (dv,), dtype=q.dtype, device=q.device)
         else:
-            _need(out, "out", q.dtype, q.shape[:-1] + (dv,))
+            _fits(out, "out", q.dtype, q.shape[:-1] + (dv,))
         if lse is None and want_lse:
             lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
         elif lse is not None:
-            _need(lse, "lse", torch.float32, q.shape[:-1])
+            _fits(lse, "lse", torch.float32, q.shape[:-1])
         ws = _workspace(dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq), q.device, workspace, s)
-        _check(lib().dsa_latent_attention_decode(_addr(q), q_stride_t, _st(q4, 2), _addr(latent), n_rows // block_size,
-                                                 block_size, _addr(block_table), int(block_table.shape[1]),
-                                                 _addr(seq_lens), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], float(scale),
-                                                 _addr(out), _addr(lse), _addr(ws), ws.numel(), s),
+        _check(lib().dsa_latent_attention_decode(q.data_ptr(), qs[1] if q_len > 1 else qs[0], qs[2], latent.data_ptr(),
+                                                 n_rows // block_size, block_size, block_table.data_ptr(), max_blocks,
+                                                 seq_lens.data_ptr(), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], scale,
+                                                 out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), s),
                "dsa_latent_attention_decode")
     finally:
         _leave(held)
@@ -770,32 +780,33 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
     max_q queries a request -> (out[Tq][H][128], lse[Tq][H] f32)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor of shape (Tq, H, 192)")
-    Tq, H, dqk = (int(n) for n in q.shape)
+    Tq, H, dqk = q.shape
     _rows(q, "q", _HALF, (Tq, H, dqk))
-    Tk, d_nope, d_pe, dv = int(k_pe.shape[0]), int(k_nope.shape[-1]), int(k_pe.shape[-1]), int(v.shape[-1])
+    Tk, d_nope, d_pe, dv = k_pe.shape[0], k_nope.shape[-1], k_pe.shape[-1], v.shape[-1]
     _rows(k_nope, "k_nope", (q.dtype,), (Tk, H, d_nope))
     _rows(k_pe, "k_pe", (q.dtype,), (Tk, d_pe))
     _rows(v, "v", (q.dtype,), (Tk, H, dv))
     if d_nope + d_pe != dqk:
         raise ValueError("q's heads must be as wide as k_nope's and k_pe together")
-    _need(cu_q, "cu_q", torch.int32)
-    _need(cu_k, "cu_k", torch.int32, cu_q.shape)
+    B = cu_q.numel() - 1
+    _fits(cu_q, "cu_q", torch.int32, (B + 1,))
+    _fits(cu_k, "cu_k", torch.int32, (B + 1,))
     s, held = _enter(stream, q, k_nope, k_pe, v, cu_q, cu_k, out, lse, workspace)
     try:
         if out is None:
             out = torch.empty(Tq, H, dv, dtype=q.dtype, device=q.device)
         else:
-            _need(out, "out", q.dtype, (Tq, H, dv))
+            _fits(out, "out", q.dtype, (Tq, H, dv))
         if lse is None and want_lse:
             lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
         elif lse is not None:
-            _need(lse, "lse", torch.float32, (Tq, H))
+            _fits(lse, "lse", torch.float32, (Tq, H))
         ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s)
+        qs, ks, vs = _strides(q), _strides(k_nope), _strides(v)
         _check(lib().dsa_latent_attention_prefill(
-            _addr(q), _st(q, 0), _st(q, 1), _addr(k_nope), _st(k_nope, 0), _st(k_nope, 1), _addr(k_pe),
-            _st(k_pe, 0), _addr(v), _st(v, 0), _st(v, 1), _addr(cu_q), _addr(cu_k), int(cu_q.numel()) - 1, Tq, Tk,
-            int(max_q), H, d_nope, d_pe, dv, _DTYPES[q.dtype], int(causal), float(scale), _addr(out), _addr(lse),
-            _addr(ws), ws.numel(), s), "dsa_latent_attention_prefill")
+            q.data_ptr(), qs[0], qs[1], k_nope.data_ptr(), ks[0], ks[1], k_pe.data_ptr(), _strides(k_pe)[0], v.data_ptr(),
+            vs[0], vs[1], cu_q.data_ptr(), cu_k.data_ptr(), B, Tq, Tk, int(max_q), H, d_nope, d_pe, dv, _DTYPES[q.dtype],
+            int(causal), scale, out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), s), "dsa_latent_attention_prefill")
     finally:
         _leave(held)
     return out, lse
