@@ -88,6 +88,7 @@ _SIGNATURES = {
     "dsa_index_cache_read": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp,
                                     _vp, _i32, _vp, _sz, _vp]),
     "dsa_latent_attention_decode_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "dsa_latent_attention_prefill_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "dsa_latent_attention_decode": (_i32, [_vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
                                            _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
     "dsa_latent_attention_prefill": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
@@ -773,6 +774,10 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     return out, lse
 
 
+def dsa_latent_attention_prefill_workspace_bytes(B: int, Tq: int, Tk: int, max_q: int, H: int) -> int:
+    return int(lib().dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H))
+
+
 def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, causal: bool = True,
                                  out=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
     """Latent attention of ragged prefills (expanded form): q[Tq][H][192], k_nope[Tk][H][128], k_pe[Tk][64],
@@ -801,6 +806,8 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
             lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
         elif lse is not None:
             _fits(lse, "lse", torch.float32, (Tq, H))
+        if workspace is None:
+            workspace = _workspace(dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H), q.device, None, s)
         ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s)
         qs, ks, vs = _strides(q), _strides(k_nope), _strides(v)
         _check(lib().dsa_latent_attention_prefill(

@@ -359,7 +359,7 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
                                                void* workspace, size_t workspace_bytes, void* stream) {
   if (!q || !latent || !block_table || !seq_lens || !out) return DSA_ERR_INVALID;
   if (B < 1 || q_len < 1 || Hq < 1 || n_blocks < 1 || block_size < 1 || max_blocks < 1) return DSA_ERR_INVALID;
-  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX ||
+  if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX - 64 ||  // (a key tile ends past the last key)
       static_cast<int64_t>(n_blocks) * block_size > INT32_MAX)
     return DSA_ERR_INVALID;
   if (!good_scale(scale) || !wide_strides(q_stride_t, q_stride_h)) return DSA_ERR_INVALID;
@@ -375,6 +375,13 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
                              max_blocks, seq_lens, B, q_len, Hq, scale, out, lse,
                              static_cast<WsHeader*>(workspace), wait_budget_ns(), sms};
   return launch_latent_decode(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+DSA_API size_t dsa_latent_attention_prefill_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t max_q, int32_t H) {
+  if (B < 1 || B > 65535 || Tq < 0 || Tk < 0 || max_q < 0 || H < 1 || H > 65535) return 0;
+  const int sms = current_num_sms();
+  if (sms < 1) return 0;
+  return latent_prefill_workspace_bytes(B, Tq, Tk, max_q, H, sms);
 }
 
 DSA_API dsa_status dsa_latent_attention_prefill(
@@ -401,7 +408,7 @@ DSA_API dsa_status dsa_latent_attention_prefill(
   const LatentPrefillParams p{q, q_stride_t, q_stride_h, k_nope, k_stride_t, k_stride_h, k_pe, pe_stride_t,
                               v, v_stride_t, v_stride_h, cu_q, cu_k, B, Tq, Tk, max_q, H, causal != 0, scale,
                               out, lse, static_cast<WsHeader*>(workspace), wait_budget_ns(), sms};
-  return launch_latent_prefill(p, dtype, static_cast<cudaStream_t>(stream));
+  return launch_latent_prefill(p, workspace_bytes, dtype, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API size_t dsa_indexcache_workspace_bytes(const dsa_indexer_shape* shape) {

@@ -421,10 +421,10 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         if (seg > 0) ok = mbar_wait_warp(&sm.seg_done, (seg - 1) & 1, ctl, DETAIL_WAIT_ACCEMPTY);
         if (mine) {
           if (t_first == 0 && te == nt) {
-            sm.inv[row] = l > 0.0f ? 1.0f / l : 0.0f;
+            sm.inv[row] = l != 0.0f ? 1.0f / l : 0.0f;
             if (p.lse && r < R)
               p.lse[static_cast<int64_t>(b) * R + r] =
-                  l > 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+                  l != 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
           } else {
             float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
             ml[row] = m;
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const float f = sm.inv[h0 + e];
               if (ht * HT + h0 + e < R)
-                out[e * kLdDv] = f > 0.0f ? ld_round<DT>(__uint_as_float(o[k][e]) * f) : static_cast<uint16_t>(0);
+                out[e * kLdDv] = f != 0.0f ? ld_round<DT>(__uint_as_float(o[k][e]) * f) : static_cast<uint16_t>(0);
             }
           } else {
             float* dst = part + (static_cast<int64_t>(h0 / 4) * kLdDv + dim) * 4;
@@ -641,10 +641,10 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
       }
 #pragma unroll
       for (int off = 1; off < kPer; off *= 2) L += __shfl_xor_sync(0xFFFFFFFFu, L, off);
-      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      const float inv = L != 0.0f ? 1.0f / L : 0.0f;
       for (int c = c_first; c < ns; c += kPer) wt[c * HT + row] *= inv;
       if (lse && blockIdx.z == 0 && c_first == 0 && row < rows)
-        lse[row] = L > 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+        lse[row] = L != 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
     }
     __syncthreads();
     {

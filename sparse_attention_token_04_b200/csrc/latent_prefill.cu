@@ -20,6 +20,7 @@
 //
 // Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
 // take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
+#include <algorithm>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -35,6 +36,7 @@ constexpr int kLpThreads = 320;
 constexpr int kLpBlock = kLpTile * 128;      // 16 KB: 128 rows x 64 dims
 constexpr int kLpKRing = 4;                  // blocks of the K ring (a tile has three)
 constexpr float kLpLazy = 6.0f;              // log2 growth of a row's maximum that is left unscaled
+constexpr int kLpMinTiles = 2, kLpMaxSplits = 32;
 
 struct LpSmem {
   uint8_t q[2][3][kLpBlock];
@@ -52,9 +54,34 @@ struct LpParams {
   float scale, scale_log2;
   void* out;
   float* lse;
+  int32_t n_blocks, splits;                  // 256-query blocks of a request, CTAs that may share one
+  float* part;                               // [request][block][head][split][32][256][4]: unnormalised O, four
+                                             // dims of a row together (lanes have a row each)
+  float2* ml;                                // [request][block][head][split][256] m, l
   WsHeader* hdr;
   uint64_t budget_ns;
 };
+
+// One 256-query block of a request.
+struct LpBlock {
+  int q0, nq, k0, nk, i0;
+  bool bad, none;                            // bad offsets; no queries in this block
+  // Keys that query i of the request sees.
+  __device__ __forceinline__ int sees(int i, int causal) const { return causal ? max(0, min(nk, nk - nq + 1 + i)) : nk; }
+  // Key tiles of query tile w.
+  __device__ __forceinline__ int tiles(int w, int causal) const {
+    const int first = i0 + w * kLpTile, last = min(first + kLpTile, nq) - 1;
+    return first < nq ? (sees(last, causal) + kLpTile - 1) / kLpTile : 0;
+  }
+};
+__device__ __forceinline__ LpBlock lp_block(const LpParams& p, int b, int qb) {
+  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
+  const bool bad = q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk || q1 - q0 > p.max_q;
+  const int i0 = qb * 2 * kLpTile;
+  return {q0, q1 - q0, k0, k1 - k0, i0, bad, i0 >= q1 - q0};
+}
+// CTAs among which the n key tiles of a block are split: each has kLpMinTiles at least.
+__device__ __forceinline__ int lp_parts(const LpParams& p, int n) { return max(1, min(p.splits, n / kLpMinTiles)); }
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
@@ -67,7 +94,13 @@ __device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
   }
 }
 
+// In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
+// are 2^-32 of the largest (and the largest, 2^(8 + kLpLazy), stays far inside its range).
 template <int DT>
+constexpr float kLpShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
+
+// kSplit: a block's key tiles are shared by up to p.splits CTAs.
+template <int DT, bool kSplit>
 __global__ void __launch_bounds__(kLpThreads, 1)
     latent_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                           const __grid_constant__ CUtensorMap map_pe, const __grid_constant__ CUtensorMap map_v,
@@ -76,24 +109,21 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   LpSmem& sm = *reinterpret_cast<LpSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x, b = blockIdx.z;
+  const int h = blockIdx.x, b = kSplit ? blockIdx.z / p.splits : blockIdx.z, split = kSplit ? blockIdx.z % p.splits : 0;
   const int qb = gridDim.y - 1 - blockIdx.y;  // the longest rows of a causal call first
 
-  const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1], k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
-  if (q0 < 0 || q1 < q0 || q1 > p.Tq || k0 < 0 || k1 < k0 || k1 > p.Tk || q1 - q0 > p.max_q) {
+  const LpBlock u = lp_block(p, b, qb);
+  if (u.bad) {
     if (tid == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SEQ_LEN);
     return;
   }
-  const int nq = q1 - q0, nk = k1 - k0, i0 = qb * 2 * kLpTile;
-  if (i0 >= nq) return;
-  // Keys that query i of the request sees, and the key tiles of each query tile.
-  auto sees = [&](int i) { return p.causal ? max(0, min(nk, nk - nq + 1 + i)) : nk; };
-  int nt[2];
-#pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const int first = i0 + w * kLpTile, last = min(first + kLpTile, nq) - 1;
-    nt[w] = first < nq ? (sees(last) + kLpTile - 1) / kLpTile : 0;
-  }
+  if (u.none) return;
+  // This CTA's key tiles [j0, j0 + n_tiles); from here on keys are counted from the first of them.
+  const int all = max(u.tiles(0, p.causal), u.tiles(1, p.causal)), parts = kSplit ? lp_parts(p, all) : 1;
+  if (split >= parts) return;
+  const int j0 = kSplit ? all * split / parts : 0, j1 = kSplit ? all * (split + 1) / parts : all, skip = j0 * kLpTile;
+  const int q0 = u.q0, nq = u.nq, i0 = u.i0, k0 = u.k0 + skip, nk = u.nk - skip;
+  const int nt[2] = {max(0, min(u.tiles(0, p.causal), j1) - j0), max(0, min(u.tiles(1, p.causal), j1) - j0)};
   const int n_tiles = max(nt[0], nt[1]);
 
   if (tid == 0) {
@@ -238,10 +268,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const int row = (warp & 3) * 32 + lane, first = i0 + w * kLpTile + (warp & 3) * 32, i = first + lane;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * 128 + lanes;
-    const int n_row = sees(i), n_warp = sees(first);
-    // In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
-    // are 2^-32 of the largest (and the largest, 2^(8 + kLpLazy), stays far inside its range).
-    constexpr float kShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
+    const int n_row = u.sees(i, p.causal) - skip, n_warp = u.sees(first, p.causal) - skip;
+    constexpr float kShift = kLpShift<DT>;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < nt[w]; ++j) {
@@ -343,8 +371,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
     tc_fence_after();
     if (ok && first < nq) {
-      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      // A row that has seen nothing (l = 0) gets zeros; one that met a NaN keeps it.
+      const float inv = l != 0.0f ? 1.0f / l : 0.0f;
       const int64_t at = static_cast<int64_t>(q0 + i) * p.H + h;
+      const int64_t unit = ((static_cast<int64_t>(b) * p.n_blocks + qb) * p.H + h) * p.splits + split;
+      float* part = p.part + unit * 2 * kLpTile * 128 + (i - i0) * 4;
       uint16_t* o_row = static_cast<uint16_t*>(p.out) + at * 128;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
@@ -353,32 +384,115 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           tmem_ld_32x32b_x32(tO + c * 32, o);
           tmem_wait_ld_regs(o);
         }
-        if (i < nq) {
+        if (kSplit && i < nq && parts > 1) {
+          if (l != 0.0f)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + (c * 32 + e) * 2 * kLpTile) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (i < nq) {
 #pragma unroll
           for (int e = 0; e < 32; e += 8) {
             uint32_t r[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              r[u] = l > 0.0f ? pack_16<DT>(__uint_as_float(o[e + 2 * u]) * inv, __uint_as_float(o[e + 2 * u + 1]) * inv)
-                              : 0u;
+            for (int k = 0; k < 4; ++k)
+              r[k] = l != 0.0f ? pack_16<DT>(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv)
+                               : 0u;
             *reinterpret_cast<uint4*>(o_row + c * 32 + e) = make_uint4(r[0], r[1], r[2], r[3]);
           }
         }
       }
-      if (i < nq && p.lse)
-        p.lse[at] = l > 0.0f ? m * p.scale + (logf(l) - kShift * 0.69314718055994531f) : -INFINITY;
+      if (kSplit && i < nq && parts > 1)
+        p.ml[unit * 2 * kLpTile + (i - i0)] = make_float2(m, l);
+      else if (i < nq && p.lse)
+        p.lse[at] = l != 0.0f ? m * p.scale + (logf(l) - kShift * 0.69314718055994531f) : -INFINITY;
     }
     tc_fence_before();
   }
   __syncthreads();
+  if constexpr (kSplit) grid_launch_dependents();
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
+// Joins the split blocks: with M the largest m of a row, out = sum_c 2^((m_c - M) scale log2 e) O_c / L,
+// L the same sum of the l_c, lse = scale M + ln L. A CTA takes 32 rows of a block, a warp 16 of the
+// dims, a lane one row.
 template <int DT>
-static dsa_status launch_prefill_dt(const LatentPrefillParams& a, cudaStream_t stream) {
+__global__ void __launch_bounds__(256) latent_prefill_combine_kernel(const LpParams p) {
+  constexpr int kRows = 2 * kLpTile;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.x, b = blockIdx.z;
+  const int qb = blockIdx.y / (kRows / 32), row = blockIdx.y % (kRows / 32) * 32 + lane;
+  const LpBlock u = lp_block(p, b, qb);
+  if (u.bad || u.i0 + row - lane >= u.nq) return;
+  const int parts = lp_parts(p, max(u.tiles(0, p.causal), u.tiles(1, p.causal)));
+  if (parts == 1) return;                     // (its CTA has written the results)
+  grid_dependency_wait();
+  if (u.i0 + row >= u.nq) return;
+  const int64_t unit = ((static_cast<int64_t>(b) * p.n_blocks + qb) * p.H + h) * p.splits * kRows;
+  const float2* ml = p.ml + unit + row;
+  float M = -INFINITY, L = 0.0f;
+  uint32_t live = 0;                          // parts that have seen something of this row (others write no O)
+#pragma unroll 8
+  for (int c = 0; c < parts; ++c) {
+    const float2 v = ml[c * kRows];
+    M = fmaxf(M, v.x);
+    live |= (v.y != 0.0f ? 1u : 0u) << c;
+  }
+  float acc[16] = {};
+  const float* src = p.part + unit * 128 + (warp * 4 * kRows + row) * 4;
+#pragma unroll 4
+  for (int c = 0; c < parts; ++c) {
+    const bool seen = live >> c & 1;
+    float4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = seen ? __ldcs(reinterpret_cast<const float4*>(src + (static_cast<int64_t>(c) * 32 + k) * kRows * 4))
+                  : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float2 v = ml[c * kRows];
+    const float f = seen ? exp2f((v.x - M) * p.scale_log2) : 0.0f;
+    L += f * v.y;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[4 * k] = fmaf(f, o[k].x, acc[4 * k]);
+      acc[4 * k + 1] = fmaf(f, o[k].y, acc[4 * k + 1]);
+      acc[4 * k + 2] = fmaf(f, o[k].z, acc[4 * k + 2]);
+      acc[4 * k + 3] = fmaf(f, o[k].w, acc[4 * k + 3]);
+    }
+  }
+  const float inv = L != 0.0f ? 1.0f / L : 0.0f;
+  const int64_t at = static_cast<int64_t>(u.q0 + u.i0 + row) * p.H + h;
+  uint32_t out[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = pack_16<DT>(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * 128 + warp * 16);
+  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  if (warp == 0 && p.lse)
+    p.lse[at] = L != 0.0f ? M * p.scale + (logf(L) - kLpShift<DT> * 0.69314718055994531f) : -INFINITY;
+}
+
+static int64_t lp_blocks(int max_q, int Tq) { return (std::min(max_q, Tq) + 2 * kLpTile - 1) / (2 * kLpTile); }
+
+// CTAs that may share a block's keys: as many as fill the SMs once, where the blocks of all requests and
+// heads would leave half of them idle.
+static int lp_splits(int B, int Tq, int Tk, int max_q, int H, int num_sms) {
+  const int64_t units = lp_blocks(max_q, Tq) * B * H, tiles = (Tk + kLpTile - 1) / kLpTile;
+  // (Short requests stay whole: their keys' join would cost what their split saves.)
+  if (units < 1 || tiles < 2ll * kLpMinTiles * B) return 1;
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_sms / units, tiles / kLpMinTiles, kLpMaxSplits})));
+}
+
+size_t latent_prefill_workspace_bytes(int B, int Tq, int Tk, int max_q, int H, int num_sms) {
+  const int splits = lp_splits(B, Tq, Tk, max_q, H, num_sms);
+  if (splits == 1) return DSA_WS_HEADER_BYTES;
+  const size_t rows = static_cast<size_t>(lp_blocks(max_q, Tq)) * B * H * splits * 2 * kLpTile;
+  return DSA_WS_HEADER_BYTES + rows * (128 + 2) * sizeof(float);
+}
+
+template <int DT>
+static dsa_status launch_prefill_dt(const LatentPrefillParams& a, int splits, cudaStream_t stream) {
   CUtensorMap mq, mk, mpe, mv;
   // With no keys at all no key box is loaded: any valid map does.
   const bool none = a.Tk == 0;
@@ -388,19 +502,39 @@ static dsa_status launch_prefill_dt(const LatentPrefillParams& a, cudaStream_t s
       !encode_tmap_3d_16(&mpe, none ? a.q : a.k_pe, 64, 1, 64, Tk, a.pes_t, 64, kLpTile) ||
       !encode_tmap_3d_16(&mv, none ? a.q : a.v, 128, a.H, a.vs_h, Tk, a.vs_t, 64, kLpTile))
     return DSA_ERR_CUDA;
+  const int blocks = static_cast<int>(lp_blocks(a.max_q, a.Tq));
+  float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.hdr) + DSA_WS_HEADER_BYTES);
+  float* ml = part + static_cast<size_t>(blocks) * a.B * a.H * splits * 2 * kLpTile * 128;
   const LpParams p{a.cu_q, a.cu_k, a.Tq, a.Tk, a.max_q, a.H, a.causal, a.scale, a.scale * 1.4426950408889634f,
-                   a.out, a.lse, a.hdr, a.budget_ns};
+                   a.out, a.lse, blocks, splits, part, reinterpret_cast<float2*>(ml), a.hdr, a.budget_ns};
   const size_t smem = sizeof(LpSmem) + 1024;
   static_assert(sizeof(LpSmem) + 1024 <= 227 * 1024, "shared memory");
-  if (!allow_shared<latent_prefill_kernel<DT>>(smem)) return DSA_ERR_CUDA;
-  const dim3 grid(a.H, (a.max_q + 2 * kLpTile - 1) / (2 * kLpTile), a.B);
-  latent_prefill_kernel<DT><<<grid, kLpThreads, smem, stream>>>(mq, mk, mpe, mv, p);
-  return cuda_status(cudaGetLastError());
+  const auto kernel = splits > 1 ? latent_prefill_kernel<DT, true> : latent_prefill_kernel<DT, false>;
+  if (!allow_shared<latent_prefill_kernel<DT, true>>(smem) || !allow_shared<latent_prefill_kernel<DT, false>>(smem))
+    return DSA_ERR_CUDA;
+  kernel<<<dim3(a.H, blocks, a.B * splits), kLpThreads, smem, stream>>>(mq, mk, mpe, mv, p);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  if (splits == 1) return DSA_OK;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.H, blocks * (2 * kLpTile / 32), a.B);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, latent_prefill_combine_kernel<DT>, p));
 }
 
-dsa_status launch_latent_prefill(const LatentPrefillParams& a, int dtype, cudaStream_t stream) {
-  return dtype == DSA_DTYPE_BF16 ? launch_prefill_dt<DSA_DTYPE_BF16>(a, stream)
-                                 : launch_prefill_dt<DSA_DTYPE_F16>(a, stream);
+dsa_status launch_latent_prefill(const LatentPrefillParams& a, size_t workspace_bytes, int dtype, cudaStream_t stream) {
+  if (lp_blocks(a.max_q, a.Tq) > 65535) return DSA_ERR_UNSUPPORTED;
+  // A workspace of the header alone leaves the blocks whole.
+  const int splits = workspace_bytes < latent_prefill_workspace_bytes(a.B, a.Tq, a.Tk, a.max_q, a.H, a.num_sms)
+                         ? 1
+                         : lp_splits(a.B, a.Tq, a.Tk, a.max_q, a.H, a.num_sms);
+  return dtype == DSA_DTYPE_BF16 ? launch_prefill_dt<DSA_DTYPE_BF16>(a, splits, stream)
+                                 : launch_prefill_dt<DSA_DTYPE_F16>(a, splits, stream);
 }
 
 }  // namespace dsa

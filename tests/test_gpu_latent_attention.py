@@ -254,6 +254,49 @@ def test_prefill_matches_oracle(dtype, nq, nk, H, causal):
     assert (out.cpu()[outside] == 77).all() and (lse.cpu()[outside] == 77).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("nq,nk,H,causal", [
+    ([1], [4000], 1, True), ([900], [900], 1, True), ([300, 0, 5], [2500, 90, 1000], 3, True),
+    ([130], [1037], 2, False), ([700], [500], 1, True), ([257, 256], [700, 3000], 2, True), ([64], [9000], 1, True)])
+def test_prefill_of_few_queries_splits_the_keys(dtype, nq, nk, H, causal):
+    q, kv, pe, cu_q, cu_k = _prefill_case(nq, nk, H, dtype, sum(nq) + H + 1)
+    need = B.dsa_latent_attention_prefill_workspace_bytes(len(nq), q.shape[0], pe.shape[0], max(nq), H)
+    assert need > 256
+    scale, kvd = 2.0 / math.sqrt(192.0), kv.cuda()
+    out = torch.full((q.shape[0], H, DV), 77.0, dtype=dtype, device="cuda")
+    lse = torch.full((q.shape[0], H), 77.0, device="cuda")
+    ws = torch.full((need,), 0x7F, dtype=torch.uint8, device="cuda")     # partial sums of 0x7F7F7F7F, but
+    ws[:256] = 0                                                        # for the header
+    args = (q.cuda(), kvd[..., :NOPE], pe.cuda(), kvd[..., NOPE:], cu_q.cuda(), cu_k.cuda(), max(nq), scale)
+    B.dsa_latent_attention_prefill(*args, causal=causal, out=out, lse=lse, workspace=ws)
+    assert B.dsa_read_device_status(ws) == (0, 0)
+    _check_prefill(q, kv, pe, cu_q, cu_k, scale, causal, out, lse)
+    outside = torch.ones(q.shape[0], dtype=torch.bool)
+    outside[3:3 + sum(nq)] = False
+    assert (out.cpu()[outside] == 77).all() and (lse.cpu()[outside] == 77).all()
+    again, lse2 = B.dsa_latent_attention_prefill(*args, causal=causal)
+    assert torch.equal(again[3:3 + sum(nq)], out[3:3 + sum(nq)]) and torch.equal(lse2[3:3 + sum(nq)], lse[3:3 + sum(nq)])
+
+
+def test_a_visible_nan_stays_one():
+    """A query that meets a NaN or infinite score gets NaN, not zeros; the others of the call are unharmed."""
+    q, kv, pe, cu_q, cu_k = _prefill_case([600], [600], 1, torch.bfloat16, 3, extra=0)
+    q[7, 0, 5] = float("nan")
+    q[300, 0, 150] = float("inf")
+    for ws in (torch.zeros(256, dtype=torch.uint8, device="cuda"), None):
+        out, lse = B.dsa_latent_attention_prefill(q.cuda(), kv.cuda()[..., :NOPE], pe.cuda(), kv.cuda()[..., NOPE:],
+                                                  cu_q.cuda(), cu_k.cuda(), 600, 0.1, workspace=ws)
+        bad = out.isnan().all(-1).flatten().cpu()
+        assert bad.nonzero().flatten().tolist() == [7, 300] and not out[~bad].isnan().any()
+        assert torch.equal(lse.isnan().flatten().cpu(), bad)
+    qd, latent, table, seq, scale = _decode_case([700, 3], 1, 20, 64, torch.bfloat16, 11)
+    qd[0, 0, 4, 570], qd[1, 0, 19, 0] = float("nan"), float("nan")
+    out, lse = B.dsa_latent_attention_decode(qd.cuda(), latent.cuda(), table.cuda(), seq.cuda(), scale)
+    bad = out.isnan().all(-1).cpu()
+    assert bad.nonzero().tolist() == [[0, 0, 4], [1, 0, 19]] and not out.cpu()[~bad].isnan().any()
+    assert torch.equal(lse.isnan().cpu(), bad)
+
+
 def test_prefill_longer_rising_scores():
     """1500 tokens whose keys grow, so that the running maximum moves many times."""
     q, kv, pe, cu_q, cu_k = _prefill_case([1500], [1500], 2, torch.bfloat16, 4)
