@@ -427,10 +427,11 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
  * absorbed form. A request's values must be finite where any of its queries sees them. A request
  * with bad offsets or more than max_q queries is recorded as DSA_ERR_DEVICE and left out.
  * workspace: >= DSA_WS_HEADER_BYTES bytes, 256-byte aligned. With at least
- * dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H) bytes the keys of a call with few
+ * dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H, causal) bytes the keys of a call with few
  * queries and heads are split over more SMs (its sums are then taken in another order).
  */
-DSA_API size_t dsa_latent_attention_prefill_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t max_q, int32_t H);
+DSA_API size_t dsa_latent_attention_prefill_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t max_q, int32_t H,
+                                                            int32_t causal);
 
 DSA_API dsa_status dsa_latent_attention_prefill(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_nope, int64_t k_stride_t,

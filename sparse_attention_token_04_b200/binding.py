@@ -88,7 +88,7 @@ _SIGNATURES = {
     "dsa_index_cache_read": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _i64, _vp, _vp,
                                     _vp, _i32, _vp, _sz, _vp]),
     "dsa_latent_attention_decode_workspace_bytes": (_sz, [_i32, _i32, _i32]),
-    "dsa_latent_attention_prefill_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "dsa_latent_attention_prefill_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "dsa_latent_attention_decode": (_i32, [_vp, _i64, _i64, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _i32, _i32,
                                            _i32, _i32, _i32, _f32, _vp, _vp, _vp, _sz, _vp]),
     "dsa_latent_attention_prefill": (_i32, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp,
@@ -774,8 +774,9 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     return out, lse
 
 
-def dsa_latent_attention_prefill_workspace_bytes(B: int, Tq: int, Tk: int, max_q: int, H: int) -> int:
-    return int(lib().dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H))
+def dsa_latent_attention_prefill_workspace_bytes(B: int, Tq: int, Tk: int, max_q: int, H: int,
+                                                 causal: bool = True) -> int:
+    return int(lib().dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H, int(causal)))
 
 
 def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, scale: float, causal: bool = True,
@@ -807,7 +808,7 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
         elif lse is not None:
             _fits(lse, "lse", torch.float32, (Tq, H))
         if workspace is None:
-            workspace = _workspace(dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H), q.device, None, s)
+            workspace = _workspace(dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H, causal), q.device, None, s)
         ws = _workspace(DSA_WS_HEADER_BYTES, q.device, workspace, s)
         qs, ks, vs = _strides(q), _strides(k_nope), _strides(v)
         _check(lib().dsa_latent_attention_prefill(

@@ -377,11 +377,12 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
   return launch_latent_decode(p, dtype, static_cast<cudaStream_t>(stream));
 }
 
-DSA_API size_t dsa_latent_attention_prefill_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t max_q, int32_t H) {
+DSA_API size_t dsa_latent_attention_prefill_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t max_q, int32_t H,
+                                                            int32_t causal) {
   if (B < 1 || B > 65535 || Tq < 0 || Tk < 0 || max_q < 0 || H < 1 || H > 65535) return 0;
   const int sms = current_num_sms();
   if (sms < 1) return 0;
-  return latent_prefill_workspace_bytes(B, Tq, Tk, max_q, H, sms);
+  return latent_prefill_workspace_bytes(B, Tq, Tk, max_q, H, causal != 0, sms);
 }
 
 DSA_API dsa_status dsa_latent_attention_prefill(

@@ -245,7 +245,7 @@ struct LatentPrefillParams {
   uint64_t budget_ns;
   int num_sms;
 };
-size_t latent_prefill_workspace_bytes(int B, int Tq, int Tk, int max_q, int H, int num_sms);
+size_t latent_prefill_workspace_bytes(int B, int Tq, int Tk, int max_q, int H, bool causal, int num_sms);
 dsa_status launch_latent_prefill(const LatentPrefillParams& p, size_t workspace_bytes, int dtype, cudaStream_t stream);
 dsa_status launch_overlap(const int32_t* const* layer_idx, int32_t n_layers, int32_t rows,
                           int32_t topk, int32_t n_keys, uint64_t* out_counts, uint64_t* out_valid,

@@ -16,10 +16,23 @@
 //                   down the one tensor pipe in issue order.
 // Shared memory: 96 KB of Q, 64 KB of K, 64 KB of V, all [128 rows][64 dims] blocks with the 128-byte
 // swizzle. (With K two tiles and V one tile deep instead, a V tile came 1000 cycles late every time; in
-// one ring of blocks for both, V's two blocks are not neighbours and PV takes twice the MMAs.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and 384-511.
+// one ring of blocks for both, V's two blocks are not neighbours and PV takes twice the MMAs: 658 us
+// where this takes 586.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and
+// 384-511. P goes over in two halves of 64 keys, so that PV starts behind the first.
 //
-// Bound: 640 FLOP a visible pair against 512 exponentials per 128 of them: the MMAs of a key tile
-// take 2560 cycles for both query tiles, its 32768 exponentials 2048 cycles of the 16-a-cycle unit.
+// Bound: 640 FLOP a visible pair. The MMAs of a key tile take 2560 cycles for both query tiles, its
+// 32768 exponentials 2048 cycles of the 16-a-cycle unit, so the softmax hides behind the products only
+// while the two query tiles stay out of step; its chain (S read, maximum, exponentials, P written) is
+// the rest. 586 us for a prompt of 8192 tokens and 32 heads, bf16: 1173 TFLOP/s, 72% of the cuBLAS
+// burst rate. Measured against it: exponentials on the FMA pipe in part (no gain: the chain waits on
+// TMEM, not on the unit), a rolled softmax that reads S twice (600 us).
+//
+// A call with few query blocks (256 queries of one head) would leave SMs idle, so its blocks' key tiles
+// are split into parts of `chunk` tiles, which write unnormalised O, m and l, and
+// latent_prefill_combine_kernel joins them. lp_plan chooses the chunk. 100 queries behind 8000 keys, 16
+// heads: 129 us whole, 27 split; 2500 tokens of one head: 50 and 17; 2048 tokens behind 6144, 16 heads
+// (128 blocks, 49 to 64 tiles long): 149 and 133. Three requests of 1300 tokens at 8 heads, which the
+// rule leaves whole: 30.3, 36.8 split.
 #include <algorithm>
 #include <cmath>
 
@@ -36,7 +49,10 @@ constexpr int kLpThreads = 320;
 constexpr int kLpBlock = kLpTile * 128;      // 16 KB: 128 rows x 64 dims
 constexpr int kLpKRing = 4;                  // blocks of the K ring (a tile has three)
 constexpr float kLpLazy = 6.0f;              // log2 growth of a row's maximum that is left unscaled
-constexpr int kLpMinTiles = 2, kLpMaxSplits = 32;
+// Splitting: key tiles of a part at least (2500 tokens of one head: 17.3 us with two, 23.3 with one, 20.6
+// with three), tiles that a split has to save (one, two and three measure alike), parts of a block and
+// places for parts per SM (133 KB each) at most.
+constexpr int kLpMinTiles = 2, kLpMinGain = 2, kLpMaxSplits = 32, kLpMaxPlaces = 6;
 
 struct LpSmem {
   uint8_t q[2][3][kLpBlock];
@@ -54,7 +70,8 @@ struct LpParams {
   float scale, scale_log2;
   void* out;
   float* lse;
-  int32_t n_blocks, splits;                  // 256-query blocks of a request, CTAs that may share one
+  int32_t n_blocks;                          // 256-query blocks of a request, at most
+  int32_t splits, chunk;                     // CTAs that may share one, key tiles of each but the last
   float* part;                               // [request][block][head][split][32][256][4]: unnormalised O, four
                                              // dims of a row together (lanes have a row each)
   float2* ml;                                // [request][block][head][split][256] m, l
@@ -80,8 +97,8 @@ __device__ __forceinline__ LpBlock lp_block(const LpParams& p, int b, int qb) {
   const int i0 = qb * 2 * kLpTile;
   return {q0, q1 - q0, k0, k1 - k0, i0, bad, i0 >= q1 - q0};
 }
-// CTAs among which the n key tiles of a block are split: each has kLpMinTiles at least.
-__device__ __forceinline__ int lp_parts(const LpParams& p, int n) { return max(1, min(p.splits, n / kLpMinTiles)); }
+// CTAs that share the n key tiles of a block.
+__device__ __forceinline__ int lp_parts(const LpParams& p, int n) { return n <= p.chunk ? 1 : (n + p.chunk - 1) / p.chunk; }
 
 template <int DT>
 __device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
@@ -109,7 +126,9 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   LpSmem& sm = *reinterpret_cast<LpSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                           ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x, b = kSplit ? blockIdx.z / p.splits : blockIdx.z, split = kSplit ? blockIdx.z % p.splits : 0;
+  const int h = blockIdx.x, n_req = kSplit ? gridDim.z / p.splits : gridDim.z;
+  // (The full parts of all blocks come before the rests.)
+  const int b = kSplit ? blockIdx.z % n_req : blockIdx.z, split = kSplit ? blockIdx.z / n_req : 0;
   const int qb = gridDim.y - 1 - blockIdx.y;  // the longest rows of a causal call first
 
   const LpBlock u = lp_block(p, b, qb);
@@ -121,7 +140,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   // This CTA's key tiles [j0, j0 + n_tiles); from here on keys are counted from the first of them.
   const int all = max(u.tiles(0, p.causal), u.tiles(1, p.causal)), parts = kSplit ? lp_parts(p, all) : 1;
   if (split >= parts) return;
-  const int j0 = kSplit ? all * split / parts : 0, j1 = kSplit ? all * (split + 1) / parts : all, skip = j0 * kLpTile;
+  const int j0 = kSplit ? split * p.chunk : 0, j1 = kSplit ? min(all, j0 + p.chunk) : all, skip = j0 * kLpTile;
   const int q0 = u.q0, nq = u.nq, i0 = u.i0, k0 = u.k0 + skip, nk = u.nk - skip;
   const int nt[2] = {max(0, min(u.tiles(0, p.causal), j1) - j0), max(0, min(u.tiles(1, p.causal), j1) - j0)};
   const int n_tiles = max(nt[0], nt[1]);
@@ -475,24 +494,59 @@ __global__ void __launch_bounds__(256) latent_prefill_combine_kernel(const LpPar
 
 static int64_t lp_blocks(int max_q, int Tq) { return (std::min(max_q, Tq) + 2 * kLpTile - 1) / (2 * kLpTile); }
 
-// CTAs that may share a block's keys: as many as fill the SMs once, where the blocks of all requests and
-// heads would leave half of them idle.
-static int lp_splits(int B, int Tq, int Tk, int max_q, int H, int num_sms) {
-  const int64_t units = lp_blocks(max_q, Tq) * B * H, tiles = (Tk + kLpTile - 1) / kLpTile;
-  // (Short requests stay whole: their keys' join would cost what their split saves.)
-  if (units < 1 || tiles < 2ll * kLpMinTiles * B) return 1;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({num_sms / units, tiles / kLpMinTiles, kLpMaxSplits})));
+// How the key tiles of the blocks are split: parts of `chunk` tiles, `splits` of them at most.
+struct LpPlan {
+  int chunk, splits;
+};
+// The chunk with the shortest estimated run, in tiles, of a call with no more blocks than SMs, taken from
+// the average request: SMs that have no full part take the rests, each of which costs two tiles more for
+// its start and end, the join costs two for every part an SM and an empty CTA half of one. The call stays
+// whole unless that saves kLpMinGain tiles of its longest block.
+static LpPlan lp_plan(int B, int Tq, int Tk, int max_q, int H, bool causal, int num_sms) {
+  const int64_t units = lp_blocks(max_q, Tq) * B * H;
+  if (units < 1 || units > num_sms) return {0, 1};
+  const int64_t nq = (Tq + B - 1) / B, nk = (Tk + B - 1) / B, key_tiles = (Tk + kLpTile - 1) / kLpTile;
+  auto tiles = [&](int64_t i) {                 // of the block of query i
+    const int64_t sees = causal ? std::max<int64_t>(0, nk - nq + std::min(i + 2 * kLpTile, nq)) : nk;
+    return (sees + kLpTile - 1) / kLpTile;
+  };
+  int64_t total = 0, longest = 0;
+  for (int64_t i = 0; i < nq; i += 2 * kLpTile) {
+    longest = std::max(longest, tiles(i));
+    total += tiles(i);
+  }
+  // The partial sums have places for as many parts a block as the longest request could have.
+  const int64_t most = std::min<int64_t>(kLpMaxSplits, kLpMaxPlaces * num_sms / units);
+  const int64_t lo = std::max<int64_t>({kLpMinTiles, (total * B * H + num_sms - 1) / num_sms, (key_tiles + most - 1) / most});
+  int64_t best = 0, best_run = longest - kLpMinGain + 1;
+  for (int64_t chunk = lo; chunk < best_run; chunk += std::max<int64_t>(1, lo / 32)) {
+    int64_t full = 0, rests = 0, rest_tiles = 0, parts = 0;
+    for (int64_t i = 0; i < nq; i += 2 * kLpTile) {
+      const int64_t n = tiles(i);
+      full += n / chunk;
+      rests += n % chunk ? 1 : 0;
+      rest_tiles += n % chunk;
+      parts += n > chunk ? (n + chunk - 1) / chunk : 0;
+    }
+    const int64_t free = num_sms - full * B * H;
+    if (free < 0 || (free == 0 && rests > 0)) continue;
+    const int64_t run = std::max(chunk, rests == 0 ? 0 : (rest_tiles + 2 * rests) * B * H / free - 2) +
+                        (2 * parts * B * H + (key_tiles + chunk - 1) / chunk * units / 2) / num_sms;
+    if (run < best_run) best = chunk, best_run = run;
+  }
+  if (best == 0) return {0, 1};
+  return {static_cast<int>(best), static_cast<int>((key_tiles + best - 1) / best)};
 }
 
-size_t latent_prefill_workspace_bytes(int B, int Tq, int Tk, int max_q, int H, int num_sms) {
-  const int splits = lp_splits(B, Tq, Tk, max_q, H, num_sms);
-  if (splits == 1) return DSA_WS_HEADER_BYTES;
+size_t latent_prefill_workspace_bytes(int B, int Tq, int Tk, int max_q, int H, bool causal, int num_sms) {
+  const int splits = lp_plan(B, Tq, Tk, max_q, H, causal, num_sms).splits;
+  if (splits <= 1) return DSA_WS_HEADER_BYTES;
   const size_t rows = static_cast<size_t>(lp_blocks(max_q, Tq)) * B * H * splits * 2 * kLpTile;
   return DSA_WS_HEADER_BYTES + rows * (128 + 2) * sizeof(float);
 }
 
 template <int DT>
-static dsa_status launch_prefill_dt(const LatentPrefillParams& a, int splits, cudaStream_t stream) {
+static dsa_status launch_prefill_dt(const LatentPrefillParams& a, LpPlan plan, cudaStream_t stream) {
   CUtensorMap mq, mk, mpe, mv;
   // With no keys at all no key box is loaded: any valid map does.
   const bool none = a.Tk == 0;
@@ -502,11 +556,11 @@ static dsa_status launch_prefill_dt(const LatentPrefillParams& a, int splits, cu
       !encode_tmap_3d_16(&mpe, none ? a.q : a.k_pe, 64, 1, 64, Tk, a.pes_t, 64, kLpTile) ||
       !encode_tmap_3d_16(&mv, none ? a.q : a.v, 128, a.H, a.vs_h, Tk, a.vs_t, 64, kLpTile))
     return DSA_ERR_CUDA;
-  const int blocks = static_cast<int>(lp_blocks(a.max_q, a.Tq));
+  const int blocks = static_cast<int>(lp_blocks(a.max_q, a.Tq)), splits = plan.splits;
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.hdr) + DSA_WS_HEADER_BYTES);
   float* ml = part + static_cast<size_t>(blocks) * a.B * a.H * splits * 2 * kLpTile * 128;
   const LpParams p{a.cu_q, a.cu_k, a.Tq, a.Tk, a.max_q, a.H, a.causal, a.scale, a.scale * 1.4426950408889634f,
-                   a.out, a.lse, blocks, splits, part, reinterpret_cast<float2*>(ml), a.hdr, a.budget_ns};
+                   a.out, a.lse, blocks, splits, plan.chunk, part, reinterpret_cast<float2*>(ml), a.hdr, a.budget_ns};
   const size_t smem = sizeof(LpSmem) + 1024;
   static_assert(sizeof(LpSmem) + 1024 <= 227 * 1024, "shared memory");
   const auto kernel = splits > 1 ? latent_prefill_kernel<DT, true> : latent_prefill_kernel<DT, false>;
@@ -529,12 +583,12 @@ static dsa_status launch_prefill_dt(const LatentPrefillParams& a, int splits, cu
 
 dsa_status launch_latent_prefill(const LatentPrefillParams& a, size_t workspace_bytes, int dtype, cudaStream_t stream) {
   if (lp_blocks(a.max_q, a.Tq) > 65535) return DSA_ERR_UNSUPPORTED;
-  // A workspace of the header alone leaves the blocks whole.
-  const int splits = workspace_bytes < latent_prefill_workspace_bytes(a.B, a.Tq, a.Tk, a.max_q, a.H, a.num_sms)
-                         ? 1
-                         : lp_splits(a.B, a.Tq, a.Tk, a.max_q, a.H, a.num_sms);
-  return dtype == DSA_DTYPE_BF16 ? launch_prefill_dt<DSA_DTYPE_BF16>(a, splits, stream)
-                                 : launch_prefill_dt<DSA_DTYPE_F16>(a, splits, stream);
+  // A workspace without room for the parts leaves the blocks whole.
+  LpPlan plan{0, 1};
+  if (workspace_bytes >= latent_prefill_workspace_bytes(a.B, a.Tq, a.Tk, a.max_q, a.H, a.causal, a.num_sms))
+    plan = lp_plan(a.B, a.Tq, a.Tk, a.max_q, a.H, a.causal, a.num_sms);
+  return dtype == DSA_DTYPE_BF16 ? launch_prefill_dt<DSA_DTYPE_BF16>(a, plan, stream)
+                                 : launch_prefill_dt<DSA_DTYPE_F16>(a, plan, stream);
 }
 
 }  // namespace dsa

@@ -260,7 +260,7 @@ def test_prefill_matches_oracle(dtype, nq, nk, H, causal):
     ([130], [1037], 2, False), ([700], [500], 1, True), ([257, 256], [700, 3000], 2, True), ([64], [9000], 1, True)])
 def test_prefill_of_few_queries_splits_the_keys(dtype, nq, nk, H, causal):
     q, kv, pe, cu_q, cu_k = _prefill_case(nq, nk, H, dtype, sum(nq) + H + 1)
-    need = B.dsa_latent_attention_prefill_workspace_bytes(len(nq), q.shape[0], pe.shape[0], max(nq), H)
+    need = B.dsa_latent_attention_prefill_workspace_bytes(len(nq), q.shape[0], pe.shape[0], max(nq), H, causal)
     assert need > 256
     scale, kvd = 2.0 / math.sqrt(192.0), kv.cuda()
     out = torch.full((q.shape[0], H, DV), 77.0, dtype=dtype, device="cuda")
