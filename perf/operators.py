@@ -217,6 +217,9 @@ def prepare(case, seed):
         nbytes = B.DSA_WS_HEADER_BYTES
         if op == "decode":
             nbytes = B.dsa_latent_attention_decode_workspace_bytes(case["B"], case["q_len"], case["Hq"])
+        elif op == "prefill":
+            nbytes = B.dsa_latent_attention_prefill_workspace_bytes(case["B"], s["q"].shape[0], s["k_pe"].shape[0],
+                                                                    s["max_q"], case["H"])
         s["ws"] = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
     return s
 
