@@ -14,15 +14,25 @@
 // products: as K (dims contiguous, K-major) and as V^T (the same bytes, M-major), so every latent is
 // fetched once. O^T has the dims on TMEM lanes and the rows on columns: 4 * HT columns, which is what
 // leaves room beside it (512 dims of 64 rows in 32 bits are half of TMEM).
-//   warps 0-3  the queries of each segment into shared memory; softmax (thread = row, warps 0 and 1
-//              at most); O^T rescaled (thread = dim) only when some row's maximum has grown by more
-//              than 2^kLdLazy; the segment's outputs;
-//   warp 4     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
+//   warps 0-3  softmax of 16 rows each (S of a 64-row MMA lies on the first 16 lanes of each TMEM
+//              quarter), as many of them as the row tile needs;
+//   warps 4-7  the queries of each segment into shared memory, O^T rescaled (thread = dim) only when
+//              some row's maximum has grown by more than 2^kLdLazy, the segment's results;
+//   warp 8     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
 //   warp 9     one thread issues the QK products, up to three tiles ahead of the softmax;
 //   warp 10    one thread issues the PV products. (With both in one thread the tensor core idled while
-//              that thread looked at its barriers.)
-// Bound by HBM for up to 64 rows a request (1152 B a key); with 128 rows the products (278528 FLOP a
-// key) take as long as the bytes.
+//              that thread looked at its barriers: 361 us instead of 356 on the long case below.)
+//
+// Row tiles of 16, 32 or 64 rows: the fewest rows that hold a request's. 16 requests of 8000 keys: 36 us
+// at 16 rows and 39 at 32, where tiles of 64 rows take 46 for both; 4 requests of 900 keys, 16 rows:
+// 12.3 and 16.7. More than 64 rows are several tiles: O^T of 128 would fill TMEM.
+//
+// Bound: for up to 64 rows a request the bytes, 1152 a key. With 128 rows the products (278528 FLOP a
+// key) would take as long, but the two row tiles pull every latent through L2 to two SMs: 32 requests of
+// 10000 to 40000 keys at 128 heads move 2 x 922 MB in 290 us, 6.3 TB/s, what a plain stream of TMA loads
+// of boxes that lie in L2 reaches (6.4). 4 requests of up to 900 keys at 16 heads: 12.9 us, which is two
+// launches and the latency of one tile's chain, TMA to result. Measured against it on the long case: two
+// softmax groups 300 us, the queries in TMEM 298, the tiles fetched into L2 ahead of time 304.
 #include <algorithm>
 #include <cmath>
 
