@@ -119,3 +119,11 @@ def test_latent_prefill_refusals(lib):
     for bad in (dict(nope=64), dict(pe_d=32), dict(dv=64), dict(dtype=2), dict(H=65536), dict(B=65536)):
         assert call(**bad) == B.DSA_ERR_UNSUPPORTED, bad
     assert call(Tq=0, q=None, out=None) == B.DSA_OK and call(max_q=0) == B.DSA_OK
+
+
+def test_latent_prefill_workspace(lib):
+    """0 for sizes that the call refuses, else the header at least."""
+    for sizes in ((0, 1, 1, 1, 1, 1), (1, -1, 1, 1, 1, 1), (1, 1, -1, 1, 1, 1), (1, 1, 1, -1, 1, 1), (1, 1, 1, 1, 0, 1),
+                  (65536, 1, 1, 1, 1, 1), (1, 1, 1, 1, 65536, 1)):
+        assert lib.dsa_latent_attention_prefill_workspace_bytes(*sizes) == 0
+    assert lib.dsa_latent_attention_prefill_workspace_bytes(1, 0, 0, 0, 1, 1) in (0, 256)   # (0 without a GPU)
