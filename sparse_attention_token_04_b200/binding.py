@@ -513,6 +513,8 @@ _HALF = (torch.bfloat16, torch.float16)
 
 def _rows(t, name: str, dtypes, shape) -> None:
     """A CUDA tensor of one of `dtypes` whose last dimension is contiguous (other strides are free)."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype in dtypes and t.shape == shape and t.stride(-1) == 1:
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
@@ -525,8 +527,8 @@ def _rows(t, name: str, dtypes, shape) -> None:
 
 def _strides(t):
     """Strides in elements; that of a dimension of one entry says nothing and is taken as 8."""
-    st = t.stride()
-    return tuple(8 if n == 1 else k for n, k in zip(t.shape, st)) if 1 in t.shape else st
+    st, shape = t.stride(), t.shape
+    return [8 if n == 1 else k for n, k in zip(shape, st)] if 1 in shape else st
 
 
 def _fits(t, name: str, dtype, shape) -> None:
@@ -617,7 +619,7 @@ def dsa_rotary(x, positions, inv_freq, interleaved: bool = False, rot_offset: in
     s, held = _enter(stream, x, positions, inv_freq, out)
     try:
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = x.new_empty((T, H, d))
         else:
             _rows(out, "out", (x.dtype,), x.shape)
         xs, os_ = _strides(x), _strides(out)
@@ -642,11 +644,11 @@ def dsa_index_quantise(x, positions=None, inv_freq=None, interleaved: bool = Fal
     s, held = _enter(stream, x, positions, inv_freq, codes, scale, workspace)
     try:
         if codes is None:
-            codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+            codes = x.new_empty((T, H, d) if x.dim() == 3 else (T, d), dtype=torch.uint8)
         else:
             _fits(codes, "codes", torch.uint8, x.shape)
         if scale is None:
-            scale = torch.empty(T, dtype=torch.float32, device=x.device)
+            scale = x.new_empty((T,), dtype=torch.float32)
         else:
             _fits(scale, "scale", torch.float32, (T,))
         ws = _workspace(DSA_WS_HEADER_BYTES, x.device, workspace, s)
@@ -683,6 +685,8 @@ def dsa_index_cache_write(x, slots, k_cache, k_scale_cache, positions=None, inv_
                                            ws.data_ptr(), ws.numel(), s), "dsa_index_cache_write")
     finally:
         _leave(held)
+
+
 def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: int, starts=None,
                          want_codes: bool = True, values=None, out_codes=None, out_scale=None, out_values=None,
                          workspace=None, stream=None):
@@ -702,23 +706,22 @@ def dsa_index_cache_read(k_cache, k_scale_cache, block_table, cu_rows, total: in
         values = out_values.dtype
     if values is not None and values not in _DTYPES:
         raise ValueError(f"values must be one of {[str(t) for t in _DTYPES]}, got {values}")
-    dev = k_cache.device
     s, held = _enter(stream, k_cache, k_scale_cache, block_table, cu_rows, starts, out_codes, out_scale,
                       out_values, workspace)
     try:
-        if want_codes and out_codes is None:
-            out_codes = torch.empty(total, d, dtype=torch.uint8, device=dev)
-        if want_codes and out_scale is None:
-            out_scale = torch.empty(total, dtype=torch.float32, device=dev)
-        if values is not None and out_values is None:
-            out_values = torch.empty(total, d, dtype=values, device=dev)
         if out_codes is not None:
             _fits(out_codes, "out_codes", torch.uint8, (total, d))
+        elif want_codes:
+            out_codes = k_cache.new_empty((total, d))
         if out_scale is not None:
             _fits(out_scale, "out_scale", torch.float32, (total,))
+        elif want_codes:
+            out_scale = k_scale_cache.new_empty((total,))
         if out_values is not None:
             _fits(out_values, "out_values", values, (total, d))
-        ws = _workspace(DSA_WS_HEADER_BYTES, dev, workspace, s)
+        elif values is not None:
+            out_values = k_cache.new_empty((total, d), dtype=values)
+        ws = _workspace(DSA_WS_HEADER_BYTES, k_cache.device, workspace, s)
         _check(lib().dsa_index_cache_read(k_cache.data_ptr(), k_scale_cache.data_ptr(), n_blocks, block_size, d,
                                           block_table.data_ptr(), max_blocks, _addr(starts), cu_rows.data_ptr(), B,
                                           total, _addr(out_codes), _addr(out_scale), _addr(out_values),
@@ -741,12 +744,15 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     [B][Hq] f32)."""
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a tensor of shape (B, q_len, Hq, 576) or (B, Hq, 576)")
-    q4 = q if q.dim() == 4 else q[:, None]
-    B, q_len, Hq, dqk = q4.shape
-    _rows(q, "q", _HALF, q.shape)
-    if B > 1 and q_len > 1 and q4.stride(0) != q_len * q4.stride(1):
+    shape = q.shape
+    _rows(q, "q", _HALF, shape)
+    st = _strides(q)
+    B, q_len, Hq, dqk = shape if len(shape) == 4 else (shape[0], 1, shape[1], shape[2])
+    if B > 1 and q_len > 1 and st[0] != q_len * st[1]:
         raise ValueError("q's tokens must be evenly spaced over its requests")
-    qs = _strides(q4)
+    # (..., q_len, Hq) of the outputs, and the stride from one token to the next
+    tokens = (B, q_len, Hq) if len(shape) == 4 else (B, Hq)
+    q_stride_t = st[1] if q_len > 1 else st[0]
     n_rows, max_blocks, dv = latent.shape[0], block_table.shape[-1], 512
     _fits(latent, "latent", q.dtype, (n_rows, dqk))
     _fits(block_table, "block_table", torch.int32, (B, max_blocks))
@@ -756,15 +762,15 @@ def dsa_latent_attention_decode(q, latent, block_table, seq_lens, scale: float, 
     s, held = _enter(stream, q, latent, block_table, seq_lens, out, lse, workspace)
     try:
         if out is None:
-            out = torch.empty(q.shape[:-1] + (dv,), dtype=q.dtype, device=q.device)
+            out = q.new_empty(tokens + (dv,))
         else:
-            _fits(out, "out", q.dtype, q.shape[:-1] + (dv,))
+            _fits(out, "out", q.dtype, tokens + (dv,))
         if lse is None and want_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+            lse = q.new_empty(tokens, dtype=torch.float32)
         elif lse is not None:
-            _fits(lse, "lse", torch.float32, q.shape[:-1])
+            _fits(lse, "lse", torch.float32, tokens)
         ws = _workspace(dsa_latent_attention_decode_workspace_bytes(B, q_len, Hq), q.device, workspace, s)
-        _check(lib().dsa_latent_attention_decode(q.data_ptr(), qs[1] if q_len > 1 else qs[0], qs[2], latent.data_ptr(),
+        _check(lib().dsa_latent_attention_decode(q.data_ptr(), q_stride_t, st[-2], latent.data_ptr(),
                                                  n_rows // block_size, block_size, block_table.data_ptr(), max_blocks,
                                                  seq_lens.data_ptr(), B, q_len, Hq, dqk, dv, _DTYPES[q.dtype], scale,
                                                  out.data_ptr(), _addr(lse), ws.data_ptr(), ws.numel(), s),
@@ -800,11 +806,11 @@ def dsa_latent_attention_prefill(q, k_nope, k_pe, v, cu_q, cu_k, max_q: int, sca
     s, held = _enter(stream, q, k_nope, k_pe, v, cu_q, cu_k, out, lse, workspace)
     try:
         if out is None:
-            out = torch.empty(Tq, H, dv, dtype=q.dtype, device=q.device)
+            out = q.new_empty((Tq, H, dv))
         else:
             _fits(out, "out", q.dtype, (Tq, H, dv))
         if lse is None and want_lse:
-            lse = torch.empty(Tq, H, dtype=torch.float32, device=q.device)
+            lse = q.new_empty((Tq, H), dtype=torch.float32)
         elif lse is not None:
             _fits(lse, "lse", torch.float32, (Tq, H))
         if workspace is None:
