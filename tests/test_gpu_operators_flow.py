@@ -185,3 +185,63 @@ def test_the_same_latent_block_in_several_requests():
     table[2, :2] = table[0, :2]
     out, lse = B.dsa_latent_attention_decode(q.cuda(), latent.cuda(), table.cuda(), seq.cuda(), scale)
     _check_decode(q, latent, table, seq, scale, 64, out, lse)
+
+
+def test_offsets_past_32_bits():
+    """Rows whose offsets, in elements and in bytes, pass 2^31 and 2^32, against the same rows in small
+    tensors: the key cache and the latents of long contexts, the index queries of a long prefill, the
+    prefill's keys."""
+    g = torch.Generator().manual_seed(1)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    # 2^32 + some bytes of key codes; slots at both ends
+    blocks = (1 << 32) // (64 * 128) + 4
+    cache = torch.empty(blocks, 64, 128, dtype=torch.uint8, device="cuda")
+    scale = torch.empty(blocks, 64, device="cuda")
+    x = torch.randn(6, 128, generator=g).to(torch.bfloat16).cuda()
+    slots = torch.tensor([0, blocks * 64 - 1, blocks * 64 - 64, (1 << 24), (1 << 25) - 1, (1 << 25)]).cuda()
+    B.dsa_index_cache_write(x, slots, cache, scale, workspace=ws)
+    codes, s = B.dsa_index_quantise(x, workspace=ws)
+    assert torch.equal(cache.view(-1, 128)[slots], codes) and torch.equal(scale.flatten()[slots], s)
+    table = torch.tensor([[blocks - 1], [1 << 19]], dtype=torch.int32, device="cuda")
+    got, gs, _ = B.dsa_index_cache_read(cache, scale, table, torch.tensor([0, 64, 65], dtype=torch.int32).cuda(), 65,
+                                        workspace=ws)
+    assert torch.equal(got[0], codes[2]) and torch.equal(got[63], codes[1]) and torch.equal(got[64], codes[5])
+    assert B.dsa_read_device_status(ws) == (0, 0)
+    del cache, scale, got
+    # latents past 2^32 bytes
+    n = (1 << 32) // (LATENT * 2) // 64 + 3
+    latent = torch.empty(n * 64, LATENT, dtype=torch.bfloat16, device="cuda")
+    small = torch.randn(128, LATENT, generator=g).to(torch.bfloat16).cuda()
+    latent[-64:], latent[:64] = small[:64], small[64:]
+    q = torch.randn(1, 1, 16, LATENT, generator=g).to(torch.bfloat16).cuda()
+    lens = torch.tensor([100], dtype=torch.int32).cuda()
+    far = torch.tensor([[n - 1, 0]], dtype=torch.int32).cuda()
+    a = B.dsa_latent_attention_decode(q, latent, far, lens, 0.05)
+    b = B.dsa_latent_attention_decode(q, small, torch.tensor([[0, 1]], dtype=torch.int32).cuda(), lens, 0.05)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    del latent
+    # queries past 2^32 bytes, the last tokens against a call of their own
+    T = (1 << 32) // (64 * 128 * 2) + 5
+    x = torch.zeros(T, 64, 128, dtype=torch.bfloat16, device="cuda")
+    x[-5:] = torch.randn(5, 64, 128, generator=g).to(torch.bfloat16).cuda()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    freq, _ = B.dsa_rotary_frequencies(64, device="cuda")
+    codes, s = B.dsa_index_quantise(x, pos, freq, workspace=ws)
+    c5, s5 = B.dsa_index_quantise(x[-5:], pos[-5:], freq, workspace=ws)
+    assert torch.equal(codes[-5:], c5) and torch.equal(s[-5:], s5)
+    y5 = B.dsa_rotary(x[-5:], pos[-5:], freq)
+    assert torch.equal(B.dsa_rotary(x, pos, freq, out=x)[-5:], y5)
+    del x, codes
+    # keys and values of a prefill in the last rows of a long tensor
+    Tk = (1 << 31) // (16 * 256) + 300
+    kv = torch.empty(Tk, 16, 256, dtype=torch.bfloat16, device="cuda")
+    pe = torch.empty(Tk, PE, dtype=torch.bfloat16, device="cuda")
+    kv[-300:] = torch.randn(300, 16, 256, generator=g).to(torch.bfloat16).cuda()
+    pe[-300:] = torch.randn(300, PE, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(40, 16, NOPE + PE, generator=g).to(torch.bfloat16).cuda()
+    cu = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()
+    a = B.dsa_latent_attention_prefill(q, kv[..., :NOPE], pe, kv[..., NOPE:], cu(0, 40), cu(Tk - 300, Tk), 40, 0.1,
+                                       workspace=ws)
+    b = B.dsa_latent_attention_prefill(q, kv[-300:, :, :NOPE], pe[-300:], kv[-300:, :, NOPE:], cu(0, 40), cu(0, 300), 40,
+                                       0.1, workspace=ws)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
