@@ -298,7 +298,9 @@ DSA_API dsa_status dsa_index_quantise(const void* x, int64_t x_stride_t, int64_t
   if (st != DSA_OK || T == 0) return st;
   const QuantParams p{r, x, x_stride_t, x_stride_h, T, H, d, nullptr, 0, codes, scale,
                       static_cast<WsHeader*>(workspace)};
-  return launch_quantise(p, dtype, static_cast<cudaStream_t>(stream));
+  const int sms = current_num_sms();
+  if (sms < 1) return DSA_ERR_CUDA;
+  return launch_quantise(p, sms, dtype, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API dsa_status dsa_index_cache_write(const void* x, int64_t x_stride_t, int64_t T, int32_t d,
@@ -317,7 +319,9 @@ DSA_API dsa_status dsa_index_cache_write(const void* x, int64_t x_stride_t, int6
   if (st != DSA_OK || T == 0) return st;
   const QuantParams p{r, x, x_stride_t, 0, T, 1, d, slots, static_cast<int64_t>(n_blocks) * block_size,
                       k_cache, k_scale_cache, static_cast<WsHeader*>(workspace)};
-  return launch_quantise(p, dtype, static_cast<cudaStream_t>(stream));
+  const int sms = current_num_sms();
+  if (sms < 1) return DSA_ERR_CUDA;
+  return launch_quantise(p, sms, dtype, static_cast<cudaStream_t>(stream));
 }
 
 DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_scale_cache,

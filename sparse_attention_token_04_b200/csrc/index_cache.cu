@@ -6,9 +6,10 @@
 // with the row's values in fp32 after the rotation (not rounded to the input's type in between),
 // both divisions IEEE fp32 and the code rounded to nearest even. Bound by HBM (long inputs) or by
 // one launch (a decode step): each value is read once and kept in registers between the row's
-// maximum and its codes. 16384 tokens of 64 heads x 128, bf16, half of each head rotated: 98 us,
-// 4.1 TB/s, and the instructions of the rotation, the maximum and the quotient then take two thirds of
+// maximum and its codes. 16384 tokens of 64 heads x 128, bf16, half of each head rotated: 87 us,
+// 4.6 TB/s, and the instructions of the rotation, the maximum and the quotient then take two thirds of
 // the issue slots. 32 keys of 128 into the cache: 4.0 us.
+#include <algorithm>
 #include <cfloat>
 #include <type_traits>
 
@@ -38,16 +39,31 @@ __device__ __forceinline__ float max_or_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
+// Two operations at a time, each rounded as the scalar one is (87 us for the row of 64 heads above, 94
+// without; the rotary kernel, bound by HBM, loses by it).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
+  return reinterpret_cast<const float2&>(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(c)));
+  return reinterpret_cast<const float2&>(r);
+}
+
 // v / scale for inv = 1 / scale, both rounded to nearest: the product's remainder is exact, and with it
 // the product is corrected to the rounded quotient (Markstein, "Computation of elementary functions on
 // the IBM RISC System/6000 processor", 1990), as long as nothing underflows, which kLeastScale sees to.
 // Checked against divisions next to every border between two codes. (Products that were checked against
 // the borders and divided where close cost more: bf16 values meet borders exactly often enough that
-// every third warp divided.)
+// every third warp divided. The uncorrected product would save 10 of 94 us.)
 constexpr float kLeastScale = 0x1p-90f;
-__device__ __forceinline__ float quotient(float v, float scale, float inv) {
-  const float q = v * inv;
-  return fmaf(fmaf(-q, scale, v), inv, q);
+__device__ __forceinline__ float2 quotient(float2 v, float scale, float inv) {
+  const float2 q = mul2(v, make_float2(inv, inv));
+  return fma2(fma2(q, make_float2(-scale, -scale), v), make_float2(inv, inv), q);
 }
 
 // Makes the compiler take the values as new: it would keep the first rotation's results, twice the
@@ -112,151 +128,235 @@ __device__ __forceinline__ float raw_max(float top, const RawVec<DT>& a, const R
   }
 }
 
-// G threads of a CTA take one row, so a CTA takes 128 / G rows: rows of up to 32 items one item a
-// thread (one warp then holds whole rows and needs no barrier for their maxima), others all 128
-// threads in up to NI passes, first over the heads' rotated items and then over the copied ones, so that
-// a pass is either for every thread. In every pass a thread has the same item of another head: it finds
-// its offsets and the eight (cos, sin) that it needs once. (16384 keys of 128: 7.6 us with 8
-// threads a row, 14.9 with 32, 59 with 128; 1024 tokens of 64 heads x 128: 8.6 us in the instance of four passes, 24 in that of 18,
-// whose registers leave room for fewer CTAs.) The values stay packed as they were loaded
-// (every load of a row is in flight at once, and five CTAs fit an SM); rotated ones are rotated twice,
-// for the maximum and for the codes.
-template <int DT, bool INTERLEAVED, int G, int NI>
-__global__ void __launch_bounds__(kQuantThreads, G > 32 && NI <= 4 ? 5 : 1)
-    index_quantise_kernel(const __grid_constant__ QuantParams p) {
+// An item's codes by corrected products.
+template <int DT, bool INTERLEAVED>
+__device__ __forceinline__ void quotient_item(RawVec<DT>& a, RawVec<DT>& b, const float2* cs, float scale, float inv,
+                                              uint8_t* out_a, uint8_t* out_b) {
+  float v[2][kVec];
+  keep_packed(a);
+  keep_packed(b);
+  unpack_raw<DT>(a, v[0]);
+  unpack_raw<DT>(b, v[1]);
+  if (cs) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) {
+      const float2 q = quotient(make_float2(v[u][e], v[u][e + 1]), scale, inv);
+      v[u][e] = q.x;
+      v[u][e + 1] = q.y;
+    }
+    *reinterpret_cast<uint2*>(u ? out_b : out_a) =
+        make_uint2(e4m3x4(v[u][0], v[u][1], v[u][2], v[u][3]), e4m3x4(v[u][4], v[u][5], v[u][6], v[u][7]));
+  }
+}
+
+// The absolute maximum of `top` and an item's values, turned where cs is given.
+template <int DT, bool INTERLEAVED>
+__device__ __forceinline__ float item_max(float top, const RawVec<DT>& a, const RawVec<DT>& b, const float2* cs) {
+  if (!cs) return raw_max<DT>(top, a, b);
+  float x[kVec], y[kVec];
+  unpack_raw<DT>(a, x);
+  unpack_raw<DT>(b, y);
+  rotary_turn<INTERLEAVED>(cs, x, y);
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) top = max_or_nan(top, x[e], y[e]);
+  return top;
+}
+
+// A row's place: its number, or its slot in the cache; -1: not written.
+__device__ __forceinline__ int64_t row_place(const QuantParams& p, int64_t t) {
+  if (t >= p.T) return -1;
+  return p.slots ? p.slots[t] : t;
+}
+__device__ __forceinline__ int64_t checked_place(const QuantParams& p, int64_t dst, bool first) {
+  if (!p.slots || (dst >= -1 && dst < p.n_slots)) return dst;
+  if (first) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SLOT);
+  return -1;
+}
+__device__ __forceinline__ float row_scale(float top) {
+  return top > 0.0f ? fmaxf(__fdiv_rn(top, 448.0f), FLT_MIN) : 1.0f;
+}
+
+// Rows of up to 32 items: G threads a row, one item a thread, 128 / G rows a CTA. A warp holds whole rows
+// and needs no barrier for their maxima.
+template <int DT, bool INTERLEAVED, int G>
+__global__ void __launch_bounds__(kQuantThreads) index_quantise_small_kernel(const __grid_constant__ QuantParams p) {
   using T = typename Elem<DT>::T;
   constexpr int kRows = kQuantThreads / G;
   extern __shared__ __align__(16) float2 cs_all[];
-  __shared__ float warp_max[kQuantThreads / 32];
-  const int half = p.r.rot / 2;
+  const int half = p.r.rot / 2, per_head = p.d / kItem;
   const int g = threadIdx.x / G, l = threadIdx.x % G;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows, t = t0 + g;
-  const int n_rot = p.r.rot / kItem, n_copy = p.d / kItem - n_rot;
-  // The thread's rotated items: item j_rot of heads h_rot, h_rot + per_rot, ... below end_rot (passes 0 to
-  // passes_rot - 1); its copied ones alike. With one item a thread they are told apart by its number.
-  int per_rot = 1, per_copy = 1, passes_rot = 0, h_rot = 0, h_copy = 0, j_rot = 0, j_copy = 0, end_rot = 0, end_copy = 0;
-  if (n_rot) {
-    per_rot = NI == 1 ? p.H : G / n_rot;
-    passes_rot = NI == 1 ? (l < p.H * n_rot) : (p.H + per_rot - 1) / per_rot;
-    h_rot = l / n_rot;
-    j_rot = l - h_rot * n_rot;
-    end_rot = h_rot < per_rot ? p.H : 0;
-  }
-  if (n_copy) {
-    const int lc = NI == 1 ? l - p.H * n_rot : l;
-    per_copy = NI == 1 ? p.H : G / n_copy;
-    h_copy = lc / n_copy;
-    j_copy = lc - h_copy * n_copy;
-    end_copy = lc >= 0 && h_copy < per_copy ? p.H : 0;
-  }
-  const Item ir = rotary_item(j_rot, p.r), ic = rotary_item(n_rot + j_copy, p.r);
-  auto head_of = [&](int k) {                   // of pass k, -1: none for this thread
-    const int head = k < passes_rot ? h_rot + k * per_rot : h_copy + (k - passes_rot) * per_copy;
-    return head < (k < passes_rot ? end_rot : end_copy) ? head : -1;
-  };
-  int64_t dst = -1;
-  if (t < p.T) {
-    dst = p.slots ? p.slots[t] : t;
-    if (p.slots && (dst < -1 || dst >= p.n_slots)) {
-      if (l == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_BAD_SLOT);
-      dst = -1;
-    }
-  }
-  RawVec<DT> ra[NI], rb[NI];
+  const int head = l / per_head < p.H ? l / per_head : -1;
+  const Item it = rotary_item(l % per_head, p.r);
+  const int64_t dst = checked_place(p, row_place(p, t), l == 0);
+  const bool mine = dst >= 0 && head >= 0;
   const T* row = static_cast<const T*>(p.x) + t * p.xs_t;
-#pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    const int head = head_of(k);
-    if (dst < 0 || head < 0) continue;
-    const T* h = row + head * p.xs_h;
-    ra[k] = load_raw<DT>(h + (k < passes_rot ? ir.a : ic.a));
-    rb[k] = load_raw<DT>(h + (k < passes_rot ? ir.b : ic.b));
+  RawVec<DT> ra, rb;
+  if (mine) {
+    ra = load_raw<DT>(row + head * p.xs_h + it.a);
+    rb = load_raw<DT>(row + head * p.xs_h + it.b);
   }
   for (int i = threadIdx.x; i < kRows * half; i += kQuantThreads) {
     const int64_t tt = t0 + i / half;
     if (tt < p.T) cs_all[i] = rotary_cos_sin(p.r.positions[tt], p.r.inv_freq[i % half], p.r);
   }
   __syncthreads();
+  const float2* cs_row = cs_all + g * half;
   float2 cs[kVec];
-  if (n_rot) {
+  if (it.f >= 0) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) cs[i] = cs_all[g * half + ir.f + i];
+    for (int i = 0; i < kVec; ++i) cs[i] = cs_row[it.f + i];
   }
   float top = 0.0f;
+  if (mine) top = item_max<DT, INTERLEAVED>(top, ra, rb, it.f >= 0 ? cs : nullptr);
 #pragma unroll
-  for (int k = 0; k < NI; ++k) {
-    if (dst < 0 || head_of(k) < 0) continue;
-    if (k < passes_rot) {
-      float a[kVec], b[kVec];
-      unpack_raw<DT>(ra[k], a);
-      unpack_raw<DT>(rb[k], b);
-      rotary_turn<INTERLEAVED>(cs, a, b);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) top = max_or_nan(top, a[e], b[e]);
-    } else {
-      top = raw_max<DT>(top, ra[k], rb[k]);
-    }
-  }
-#pragma unroll
-  for (int off = (G < 32 ? G : 32) / 2; off > 0; off >>= 1)
-    top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off), 0.0f);
-  if constexpr (G > 32) {
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < G / 32; ++w) top = max_or_nan(top, warp_max[w], 0.0f);
-  }
+  for (int off = G / 2; off > 0; off >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off), 0.0f);
   if (dst < 0) return;
   // A row with a value that is not finite: its maximum is not finite either, and is found anew by every
   // thread from the whole row.
   const bool mend = !(top <= FLT_MAX);
   if (mend) {
     if (l == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_NOT_FINITE);
-    top = finite_max<DT, INTERLEAVED>(&p, row, cs_all + g * half);
+    top = finite_max<DT, INTERLEAVED>(&p, row, cs_row);
   }
-  const float scale = top > 0.0f ? fmaxf(__fdiv_rn(top, 448.0f), FLT_MIN) : 1.0f;
-  const float inv = __fdiv_rn(1.0f, scale);
-  uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d);
-  if (mend || scale < kLeastScale) {
-#pragma unroll 1
-    for (int k = 0; k < NI; ++k) {
-      const int head = head_of(k);
-      if (head < 0) continue;
-      const Item& it = k < passes_rot ? ir : ic;
-      const T* h = row + head * p.xs_h;
-      divided_item<DT, INTERLEAVED>(h + it.a, h + it.b, it.f >= 0 ? cs_all + g * half + it.f : nullptr, scale,
-                                    out + head * p.d + it.a, out + head * p.d + it.b);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < NI; ++k) {
-      const int head = head_of(k);
-      if (head < 0) continue;
-      float v[2][kVec];
-      keep_packed(ra[k]);
-      keep_packed(rb[k]);
-      unpack_raw<DT>(ra[k], v[0]);
-      unpack_raw<DT>(rb[k], v[1]);
-      if (k < passes_rot) rotary_turn<INTERLEAVED>(cs, v[0], v[1]);
-      uint8_t* o = out + head * p.d;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) v[u][e] = quotient(v[u][e], scale, inv);
-        *reinterpret_cast<uint2*>(o + (k < passes_rot ? (u ? ir.b : ir.a) : (u ? ic.b : ic.a))) =
-            make_uint2(e4m3x4(v[u][0], v[u][1], v[u][2], v[u][3]), e4m3x4(v[u][4], v[u][5], v[u][6], v[u][7]));
-      }
-    }
+  const float scale = row_scale(top);
+  if (mine) {
+    uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d) + head * p.d;
+    if (mend || scale < kLeastScale)
+      divided_item<DT, INTERLEAVED>(row + head * p.xs_h + it.a, row + head * p.xs_h + it.b,
+                                    it.f >= 0 ? cs_row + it.f : nullptr, scale, out + it.a, out + it.b);
+    else
+      quotient_item<DT, INTERLEAVED>(ra, rb, it.f >= 0 ? cs : nullptr, scale, __fdiv_rn(1.0f, scale), out + it.a, out + it.b);
   }
   if (l == 0) p.scale[dst] = scale;
 }
 
-template <int DT, bool INTERLEAVED, int G, int NI>
-static dsa_status launch_quantise_g(const QuantParams& p, cudaStream_t stream) {
+// Larger rows: a CTA takes one row after another, in up to NI passes, first over the heads' rotated items
+// and then over the copied ones, so that a pass is either for every thread. In every pass a thread has
+// the same item of another head: it finds its offsets once. A row's values stay packed as they were
+// loaded; rotated ones are rotated twice, for the maximum and for the codes. (With the next row's
+// loads on their way while this one's are worked on, which leaves registers for four CTAs an SM instead
+// of five, the row of 64 heads below takes 99 to 124 us.) One barrier a row: in front of it a warp leaves its maximum (two
+// buffers) and the first threads the next row's (cos, sin) (three, since the rare paths read them behind
+// it).
+template <int DT, bool INTERLEAVED, int NI>
+__global__ void __launch_bounds__(kQuantThreads, NI <= 4 ? 5 : 1)
+    index_quantise_kernel(const __grid_constant__ QuantParams p) {
+  using T = typename Elem<DT>::T;
+  extern __shared__ __align__(16) float2 cs_all[];  // [3][half]
+  __shared__ float warp_max[2][kQuantThreads / 32];
+  const int half = p.r.rot / 2, l = threadIdx.x;
+  const int n_rot = p.r.rot / kItem, n_copy = p.d / kItem - n_rot;
+  // The thread's rotated items: item j_rot of heads h_rot, h_rot + per_rot, ... below end_rot (passes 0 to
+  // passes_rot - 1); its copied ones alike.
+  int per_rot = 1, per_copy = 1, passes_rot = 0, h_rot = 0, h_copy = 0, j_rot = 0, j_copy = 0, end_rot = 0, end_copy = 0;
+  if (n_rot) {
+    per_rot = kQuantThreads / n_rot;
+    passes_rot = (p.H + per_rot - 1) / per_rot;
+    h_rot = l / n_rot;
+    j_rot = l - h_rot * n_rot;
+    end_rot = h_rot < per_rot ? p.H : 0;
+  }
+  if (n_copy) {
+    per_copy = kQuantThreads / n_copy;
+    h_copy = l / n_copy;
+    j_copy = l - h_copy * n_copy;
+    end_copy = h_copy < per_copy ? p.H : 0;
+  }
+  const Item ir = rotary_item(j_rot, p.r), ic = rotary_item(n_rot + j_copy, p.r);
+  auto head_of = [&](int k) {                   // of pass k, -1: none for this thread
+    const int head = k < passes_rot ? h_rot + k * per_rot : h_copy + (k - passes_rot) * per_copy;
+    return head < (k < passes_rot ? end_rot : end_copy) ? head : -1;
+  };
+  auto turns = [&](int64_t t, float2* cs) {
+    for (int i = l; i < half; i += kQuantThreads) cs[i] = rotary_cos_sin(p.r.positions[t], p.r.inv_freq[i], p.r);
+  };
+  RawVec<DT> ra[NI], rb[NI];
+  int64_t t = blockIdx.x, place = row_place(p, t);
+  turns(t, cs_all);
+  __syncthreads();
+#pragma unroll 1
+  for (int n = 0; t < p.T; ++n, t += gridDim.x) {
+    const float2* cs_row = cs_all + n % 3 * half;
+    const int64_t next = t + gridDim.x, next_place = row_place(p, next);
+    const T* row = static_cast<const T*>(p.x) + t * p.xs_t;
+#pragma unroll
+    for (int k = 0; k < NI; ++k) {
+      const int head = head_of(k);
+      if (head < 0) continue;
+      const T* h = row + head * p.xs_h;
+      ra[k] = load_raw<DT>(h + (k < passes_rot ? ir.a : ic.a));
+      rb[k] = load_raw<DT>(h + (k < passes_rot ? ir.b : ic.b));
+    }
+    const int64_t dst = checked_place(p, place, l == 0);
+    place = next_place;
+    float2 cs[kVec];
+    if (n_rot) {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) cs[i] = cs_row[ir.f + i];
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NI; ++k)
+      if (head_of(k) >= 0) top = item_max<DT, INTERLEAVED>(top, ra[k], rb[k], k < passes_rot ? cs : nullptr);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, off), 0.0f);
+    if ((l & 31) == 0) warp_max[n & 1][l >> 5] = top;
+    if (next < p.T) turns(next, cs_all + (n + 1) % 3 * half);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kQuantThreads / 32; ++w) top = max_or_nan(top, warp_max[n & 1][w], 0.0f);
+    if (dst >= 0) {
+      // (A row with a value that is not finite: as above.)
+      const bool mend = !(top <= FLT_MAX);
+      if (mend) {
+        if (l == 0) record_error(p.hdr, DSA_ERR_DEVICE, DETAIL_NOT_FINITE);
+        top = finite_max<DT, INTERLEAVED>(&p, row, cs_row);
+      }
+      const float scale = row_scale(top);
+      uint8_t* out = p.codes + dst * (static_cast<int64_t>(p.H) * p.d);
+      if (mend || scale < kLeastScale) {
+#pragma unroll 1
+        for (int k = 0; k < NI; ++k) {
+          const int head = head_of(k);
+          if (head < 0) continue;
+          const Item& it = k < passes_rot ? ir : ic;
+          divided_item<DT, INTERLEAVED>(row + head * p.xs_h + it.a, row + head * p.xs_h + it.b,
+                                        it.f >= 0 ? cs_row + it.f : nullptr, scale, out + head * p.d + it.a,
+                                        out + head * p.d + it.b);
+        }
+      } else {
+        const float inv = __fdiv_rn(1.0f, scale);
+#pragma unroll
+        for (int k = 0; k < NI; ++k) {
+          const int head = head_of(k);
+          if (head < 0) continue;
+          uint8_t* o = out + head * p.d;
+          if (k < passes_rot) quotient_item<DT, INTERLEAVED>(ra[k], rb[k], cs, scale, inv, o + ir.a, o + ir.b);
+          else quotient_item<DT, INTERLEAVED>(ra[k], rb[k], nullptr, scale, inv, o + ic.a, o + ic.b);
+        }
+      }
+      if (l == 0) p.scale[dst] = scale;
+    }
+  }
+}
+
+template <int DT, bool INTERLEAVED, int G>
+static dsa_status launch_quantise_small(const QuantParams& p, cudaStream_t stream) {
   constexpr int kRows = kQuantThreads / G;
   const size_t smem = static_cast<size_t>(kRows) * (p.r.rot / 2) * sizeof(float2);
   const int64_t grid = (p.T + kRows - 1) / kRows;
-  index_quantise_kernel<DT, INTERLEAVED, G, NI><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
+  index_quantise_small_kernel<DT, INTERLEAVED, G><<<static_cast<unsigned>(grid), kQuantThreads, smem, stream>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int DT, bool INTERLEAVED, int NI>
+static dsa_status launch_quantise_rows(const QuantParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = static_cast<size_t>(3) * (p.r.rot / 2) * sizeof(float2);
+  const int grid = static_cast<int>(std::min<int64_t>(p.T, static_cast<int64_t>(num_sms) * (NI <= 4 ? 5 : 2)));
+  index_quantise_kernel<DT, INTERLEAVED, NI><<<grid, kQuantThreads, smem, stream>>>(p);
   return cuda_status(cudaGetLastError());
 }
 
@@ -271,26 +371,29 @@ static int quantise_passes(const QuantParams& p) {
 }
 
 template <int DT, bool INTERLEAVED>
-static dsa_status launch_quantise_t(const QuantParams& p, cudaStream_t stream) {
+static dsa_status launch_quantise_t(const QuantParams& p, int num_sms, cudaStream_t stream) {
   const int n = p.H * (p.d / kItem);
-  // Few rows are spread over more CTAs (32 keys of 128: 2.7 us, 3.3 with 8 threads a row).
-  if (n <= 32 && p.T <= kQuantFewRows) return launch_quantise_g<DT, INTERLEAVED, 32, 1>(p, stream);
-  if (n <= 8) return launch_quantise_g<DT, INTERLEAVED, 8, 1>(p, stream);
-  if (n <= 16) return launch_quantise_g<DT, INTERLEAVED, 16, 1>(p, stream);
-  if (n <= 32) return launch_quantise_g<DT, INTERLEAVED, 32, 1>(p, stream);
-  if (quantise_passes(p) <= 4) return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 4>(p, stream);
-  return launch_quantise_g<DT, INTERLEAVED, kQuantThreads, 18>(p, stream);
+  // As few threads a row as it has items (16384 keys of 128: 6.8 us with 8 threads, 14.9 with 32), but few
+  // rows are spread over more CTAs (32 keys of 128: 2.5 us with 32, 3.3 with 8). The instance of 18 passes
+  // takes any larger row, with registers for fewer CTAs (1024 tokens of 64 heads x 128: 24 us, 8.0 in the
+  // one of four).
+  if (n <= 32 && p.T <= kQuantFewRows) return launch_quantise_small<DT, INTERLEAVED, 32>(p, stream);
+  if (n <= 8) return launch_quantise_small<DT, INTERLEAVED, 8>(p, stream);
+  if (n <= 16) return launch_quantise_small<DT, INTERLEAVED, 16>(p, stream);
+  if (n <= 32) return launch_quantise_small<DT, INTERLEAVED, 32>(p, stream);
+  if (quantise_passes(p) <= 4) return launch_quantise_rows<DT, INTERLEAVED, 4>(p, num_sms, stream);
+  return launch_quantise_rows<DT, INTERLEAVED, 18>(p, num_sms, stream);
 }
 
-dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream) {
+dsa_status launch_quantise(const QuantParams& p, int num_sms, int dtype, cudaStream_t stream) {
   if (p.r.interleaved) {
-    if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, true>(p, stream);
-    if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, true>(p, stream);
-    return launch_quantise_t<DSA_DTYPE_F32, true>(p, stream);
+    if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, true>(p, num_sms, stream);
+    if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, true>(p, num_sms, stream);
+    return launch_quantise_t<DSA_DTYPE_F32, true>(p, num_sms, stream);
   }
-  if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, false>(p, stream);
-  if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, false>(p, stream);
-  return launch_quantise_t<DSA_DTYPE_F32, false>(p, stream);
+  if (dtype == DSA_DTYPE_BF16) return launch_quantise_t<DSA_DTYPE_BF16, false>(p, num_sms, stream);
+  if (dtype == DSA_DTYPE_F16) return launch_quantise_t<DSA_DTYPE_F16, false>(p, num_sms, stream);
+  return launch_quantise_t<DSA_DTYPE_F32, false>(p, num_sms, stream);
 }
 
 // ------------------------------------------------------------------------------------------

@@ -190,7 +190,7 @@ struct QuantParams {
   float* scale;
   WsHeader* hdr;
 };
-dsa_status launch_quantise(const QuantParams& p, int dtype, cudaStream_t stream);
+dsa_status launch_quantise(const QuantParams& p, int num_sms, int dtype, cudaStream_t stream);
 struct ReadParams {
   const uint8_t* k_cache;
   const float* k_scale_cache;

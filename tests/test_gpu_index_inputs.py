@@ -307,3 +307,35 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(c3, want) and torch.equal(s3, scale) and torch.equal(r3, rot)
+
+
+@pytest.mark.parametrize("dtype,H,d,rot,interleaved", [
+    (torch.bfloat16, 64, 128, 64, False), (torch.float16, 64, 128, 64, True), (torch.float32, 33, 64, 32, False),
+    (torch.bfloat16, 9, 64, 0, False), (torch.float32, 128, 128, 128, True), (torch.bfloat16, 100, 48, 16, False)])
+def test_quantise_many_large_rows(dtype, H, d, rot, interleaved):
+    """More rows than there are CTAs for, among them zero, tiny and non-finite ones: the same bits as in calls
+    of few rows, and the finite rows within the oracle's bound."""
+    T = 3100
+    x = _randn((T, H, d), H + d, dtype)
+    x[5::97] = 0
+    x[6::97] *= 2.0 ** -14
+    if dtype != torch.float16:
+        x[7::97] *= 1e-30
+    x[1000, H - 1, d - 1], x[1001, 0, 0], x[2999, H // 2, 1] = float("nan"), float("inf"), -float("inf")
+    pos = _positions(T, 3)
+    f, _ = B.dsa_rotary_frequencies(rot, device="cuda") if rot else (None, 1.0)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+    def call(a, e):
+        kw = dict(positions=pos[a:e].cuda(), inv_freq=f, interleaved=interleaved) if rot else {}
+        return B.dsa_index_quantise(x[a:e].cuda(), workspace=ws, **kw)
+
+    codes, scale = call(0, T)
+    assert B.dsa_read_device_status(ws) == (B.DSA_ERR_DEVICE, 21)
+    parts = [call(a, min(a + 100, T)) for a in range(0, T, 100)]
+    assert torch.equal(codes, torch.cat([c for c, _ in parts])) and torch.equal(scale, torch.cat([s for _, s in parts]))
+    some = [0, 1, 5, 6, 7, 739, 740, 741, 1480, 2220, 2221, 3099]
+    values = x[some].double().numpy()
+    if rot:
+        values = O.rotary(values, pos[some].numpy(), f.cpu().numpy(), interleaved)
+    _check_codes(codes[some].flatten(1), scale[some], values.reshape(len(some), -1))
