@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(256) latent_prefill_combine_kernel(const LpPar
     p.lse[at] = L != 0.0f ? M * p.scale + (logf(L) - kLpShift<DT> * 0.69314718055994531f) : -INFINITY;
 }
 
-static int64_t lp_blocks(int max_q, int Tq) { return (std::min(max_q, Tq) + 2 * kLpTile - 1) / (2 * kLpTile); }
+static int64_t lp_blocks(int max_q, int Tq) { return (static_cast<int64_t>(std::min(max_q, Tq)) + 2 * kLpTile - 1) / (2 * kLpTile); }
 
 // How the key tiles of the blocks are split: parts of `chunk` tiles, `splits` of them at most.
 struct LpPlan {
@@ -505,7 +505,9 @@ struct LpPlan {
 static LpPlan lp_plan(int B, int Tq, int Tk, int max_q, int H, bool causal, int num_sms) {
   const int64_t units = lp_blocks(max_q, Tq) * B * H;
   if (units < 1 || units > num_sms) return {0, 1};
-  const int64_t nq = (Tq + B - 1) / B, nk = (Tk + B - 1) / B, key_tiles = (Tk + kLpTile - 1) / kLpTile;
+  // (Rows outside the requests count towards Tq and Tk; max_q bounds what they can add.)
+  const int64_t nq = std::min<int64_t>((static_cast<int64_t>(Tq) + B - 1) / B, max_q);
+  const int64_t nk = (static_cast<int64_t>(Tk) + B - 1) / B, key_tiles = (static_cast<int64_t>(Tk) + kLpTile - 1) / kLpTile;
   auto tiles = [&](int64_t i) {                 // of the block of query i
     const int64_t sees = causal ? std::max<int64_t>(0, nk - nq + std::min(i + 2 * kLpTile, nq)) : nk;
     return (sees + kLpTile - 1) / kLpTile;

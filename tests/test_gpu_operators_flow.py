@@ -245,3 +245,11 @@ def test_offsets_past_32_bits():
     b = B.dsa_latent_attention_prefill(q, kv[-300:, :, :NOPE], pe[-300:], kv[-300:, :, NOPE:], cu(0, 40), cu(0, 300), 40,
                                        0.1, workspace=ws)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_prefill_workspace_of_rows_outside_requests():
+    """Rows that belong to no request cost the plan nothing: max_q bounds a request."""
+    need = B.dsa_latent_attention_prefill_workspace_bytes
+    assert need(1, 2 ** 31 - 1, 5000, 1, 1) == need(1, 1, 5000, 1, 1) > 256
+    assert need(1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 1) == 256
+    assert need(1, 1, 2 ** 31 - 1, 1, 1) < 2 ** 30
