@@ -122,12 +122,12 @@ bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, u
 }
 
 bool encode_tmap_3d_16(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint64_t row_stride,
-                       uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_outer) {
+                       uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_rows, uint32_t box_outer) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
   if (!encode) return false;
   const cuuint64_t dims[3] = {d, rows, outer};
   const cuuint64_t strides[2] = {row_stride * 2, outer_stride * 2};
-  const cuuint32_t box[3] = {box_d, 1, box_outer};
+  const cuuint32_t box[3] = {box_d, box_rows, box_outer};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -261,10 +261,10 @@ dsa_status launch_topk_merge(const float* scores, const int32_t* idx, const int3
 bool encode_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows,
                        uint32_t box_rows, uint64_t row_stride = 0);
 
-// 16-bit elements of [outer][rows][d], strides in elements; boxes of box_d x 1 x box_outer with the
-// 128-byte swizzle.
+// 16-bit elements of [outer][rows][d], strides in elements; boxes of box_d x box_rows x
+// box_outer with the 128-byte swizzle.
 bool encode_tmap_3d_16(CUtensorMap* map, const void* base, uint64_t d, uint64_t rows, uint64_t row_stride,
-                       uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_outer);
+                       uint64_t outer, uint64_t outer_stride, uint32_t box_d, uint32_t box_rows, uint32_t box_outer);
 
 // Lets a kernel use `bytes` (the same on every call) of dynamic shared memory; asked of the runtime once
 // per device.

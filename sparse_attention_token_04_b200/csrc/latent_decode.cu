@@ -18,7 +18,7 @@
 //              quarter), as many of them as the row tile needs;
 //   warps 4-7  the queries of each segment into shared memory, O^T rescaled (thread = dim) only when
 //              some row's maximum has grown by more than 2^kLdLazy, the segment's results;
-//   warp 8     TMA: nine 64-dim chunks of 4 KB a tile, into a ring of four or five tiles;
+//   warp 8     TMA: a tile as one box of nine 64-dim chunks of 4 KB, into a ring of four or five tiles;
 //   warp 9     one thread issues the QK products, up to three tiles ahead of the softmax;
 //   warp 10    one thread issues the PV products. (With both in one thread the tensor core idled while
 //              that thread looked at its barriers: 361 us instead of 356 on the long case below.)
@@ -250,9 +250,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         if (!ok) break;
         if (n_box == 1) {
           mbar_arrive_expect_tx(&sm.full[st], kLdTileBytes);
-#pragma unroll
-          for (int c = 0; c < kLdChunks; ++c)
-            tma_load_3d(ring + c * kLdSlotBytes, &map_latent, c * 64, 0, cur, &sm.full[st]);
+          tma_load_3d(ring, &map_latent, 0, cur, 0, &sm.full[st]);
         } else {
           const int boxes = min(n_box, (cn - ct * kLdKeys + p.box_rows - 1) / p.box_rows);
           mbar_arrive_expect_tx(&sm.full[st], kLdChunks * boxes * p.box_rows * 128);
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             const int first = i == 0 ? cur : box_row(cb, ct, cn, i);
 #pragma unroll 1
             for (int c = 0; c < kLdChunks; ++c)
-              tma_load_3d(ring + c * kLdSlotBytes + i * p.box_rows * 128, &map_latent, c * 64, 0, first, &sm.full[st]);
+              tma_load_3d(ring + c * kLdSlotBytes + i * p.box_rows * 128, &map_latent, 0, first, c, &sm.full[st]);
           }
         }
         if (++st == kStages) st = 0, ph ^= 1;
@@ -720,8 +718,9 @@ static dsa_status launch_decode_ht(const LatentDecodeParams& a, cudaStream_t str
   int box = kLdKeys;                            // the largest box that divides tiles and blocks
   while (a.block_size % box) box /= 2;
   CUtensorMap map;
-  if (!encode_tmap_3d_16(&map, a.latent, kLdDqk, 1, kLdDqk, static_cast<uint64_t>(a.n_blocks) * a.block_size, kLdDqk,
-                         64, box))
+  // A latent as nine chunks of 64 dims: one load brings a whole tile, chunk by chunk, where it is one box.
+  if (!encode_tmap_3d_16(&map, a.latent, 64, static_cast<uint64_t>(a.n_blocks) * a.block_size, kLdDqk, kLdChunks, 64,
+                         64, box, box == kLdKeys ? kLdChunks : 1))
     return DSA_ERR_CUDA;
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.hdr) + DSA_WS_HEADER_BYTES);
   const LdParams p{static_cast<const uint16_t*>(a.q), a.qs_t, a.qs_h, a.block_table, a.seq_lens, a.n_blocks,

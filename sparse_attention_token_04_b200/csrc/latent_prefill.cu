@@ -553,10 +553,10 @@ static dsa_status launch_prefill_dt(const LatentPrefillParams& a, LpPlan plan, c
   // With no keys at all no key box is loaded: any valid map does.
   const bool none = a.Tk == 0;
   const uint64_t Tk = none ? 1 : a.Tk;
-  if (!encode_tmap_3d_16(&mq, a.q, 192, a.H, a.qs_h, a.Tq, a.qs_t, 64, kLpTile) ||
-      !encode_tmap_3d_16(&mk, none ? a.q : a.k_nope, 128, a.H, a.ks_h, Tk, a.ks_t, 64, kLpTile) ||
-      !encode_tmap_3d_16(&mpe, none ? a.q : a.k_pe, 64, 1, 64, Tk, a.pes_t, 64, kLpTile) ||
-      !encode_tmap_3d_16(&mv, none ? a.q : a.v, 128, a.H, a.vs_h, Tk, a.vs_t, 64, kLpTile))
+  if (!encode_tmap_3d_16(&mq, a.q, 192, a.H, a.qs_h, a.Tq, a.qs_t, 64, 1, kLpTile) ||
+      !encode_tmap_3d_16(&mk, none ? a.q : a.k_nope, 128, a.H, a.ks_h, Tk, a.ks_t, 64, 1, kLpTile) ||
+      !encode_tmap_3d_16(&mpe, none ? a.q : a.k_pe, 64, 1, 64, Tk, a.pes_t, 64, 1, kLpTile) ||
+      !encode_tmap_3d_16(&mv, none ? a.q : a.v, 128, a.H, a.vs_h, Tk, a.vs_t, 64, 1, kLpTile))
     return DSA_ERR_CUDA;
   const int blocks = static_cast<int>(lp_blocks(a.max_q, a.Tq)), splits = plan.splits;
   float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(a.hdr) + DSA_WS_HEADER_BYTES);
