@@ -39,27 +39,13 @@ __device__ __forceinline__ float max_or_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return m;
 }
-// Two operations at a time, each rounded as the scalar one is (87 us for the row of 64 heads above, 94
-// without; the rotary kernel, bound by HBM, loses by it).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)));
-  return reinterpret_cast<const float2&>(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(r)
-      : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(c)));
-  return reinterpret_cast<const float2&>(r);
-}
-
 // v / scale for inv = 1 / scale, both rounded to nearest: the product's remainder is exact, and with it
 // the product is corrected to the rounded quotient (Markstein, "Computation of elementary functions on
 // the IBM RISC System/6000 processor", 1990), as long as nothing underflows, which kLeastScale sees to.
 // Checked against divisions next to every border between two codes. (Products that were checked against
 // the borders and divided where close cost more: bf16 values meet borders exactly often enough that
-// every third warp divided. The uncorrected product would save 10 of 94 us.)
+// every third warp divided. Without the correction the row of 64 heads above took 83 us, with it 94, two
+// values at a time 87; the rotary kernel, bound by HBM, gained nothing from turning two at a time.)
 constexpr float kLeastScale = 0x1p-90f;
 __device__ __forceinline__ float2 quotient(float2 v, float scale, float inv) {
   const float2 q = mul2(v, make_float2(inv, inv));

@@ -20,12 +20,15 @@
 // where this takes 586.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and
 // 384-511. P goes over in two halves of 64 keys, so that PV starts behind the first.
 //
-// Bound: 640 FLOP a visible pair. The MMAs of a key tile take 2560 cycles for both query tiles, its
-// 32768 exponentials 2048 cycles of the 16-a-cycle unit, so the softmax hides behind the products only
-// while the two query tiles stay out of step; its chain (S read, maximum, exponentials, P written) is
-// the rest. 586 us for a prompt of 8192 tokens and 32 heads, bf16: 1173 TFLOP/s, 72% of the cuBLAS
-// burst rate. Measured against it: exponentials on the FMA pipe in part (no gain: the chain waits on
-// TMEM, not on the unit), a rolled softmax that reads S twice (600 us).
+// Bound: the chain of one query tile. The MMAs of a key tile take 2560 cycles for both query tiles, but
+// S and P share columns, so a tile's next QK waits for its PV: from scores to scores its softmax (2200
+// cycles: 700 to read S and find the maximum, 1500 for the exponentials, whose unit both tiles share),
+// its own products (1280) and some 600 of hand-over follow one another, 4300 cycles in all. 580 us for a
+// prompt of 8192 tokens and 32 heads, bf16: 1190 TFLOP/s, 73% of the cuBLAS burst rate. Measured against
+// it: two threads a row (614 us: the pair's exchange and the shared unit take what the shorter rows give),
+// a quarter of the exponentials on the FMA pipe (596), P handed over in parts of 96 and 32 keys (588),
+// tiles fetched into L2 ahead of time (598), K and V blocks of 64 keys in one ring of eight (579, but 142
+// against 137 us for 2048 tokens behind 6144), a rolled softmax that reads S twice (600).
 //
 // A call with few query blocks (256 queries of one head) would leave SMs idle, so its blocks' key tiles
 // are split into parts of `chunk` tiles, which write unnormalised O, m and l, and
@@ -362,29 +365,37 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       }
       const float base = m == -INFINITY ? 0.0f : kShift - m * p.scale_log2;
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      // The numerators of 64 keys, rounded into P.
-      auto numerators = [&](int half) {
-        uint32_t packed[32];
+      // The numerators of 32 keys, rounded into P.
+      auto numerators = [&](int c) {
+        uint32_t packed[16];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const uint32_t* v = &s[half * 2 + (e >> 5)][e & 31];
-          const float p0 = exp2_fast(fmaf(__uint_as_float(v[0]), p.scale_log2, base));
-          const float p1 = exp2_fast(fmaf(__uint_as_float(v[1]), p.scale_log2, base));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                make_float2(p.scale_log2, p.scale_log2), make_float2(base, base));
+          const float p0 = exp2_fast(x.x), p1 = exp2_fast(x.y);
           sum[e & 2] += p0;
           sum[(e & 2) + 1] += p1;
           packed[e >> 1] = pack_16<DT>(p0, p1);
         }
-        tmem_st_32x32b_x32(tS + half * 32, packed);
+        tmem_st_32x32b_x16(tS + c * 16, packed);
+      };
+      auto hand_over = [&](int part) {
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready[w][half]);
+        if (lane == 0) mbar_arrive(&sm.p_ready[w][part]);
       };
-      numerators(0);
-      // (Nothing of the second half is computed before the first is on its way.)
 #pragma unroll
-      for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[2][e]), "+r"(s[3][e]));
-      numerators(1);
+      for (int c = 0; c < 4; ++c) {
+        numerators(c);
+        if (c == 1) hand_over(0);
+        // (Nothing of a chunk is computed before the one in front of it is on its way.)
+        if (c < 3) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) asm volatile("" : "+r"(s[c + 1][e]));
+        }
+      }
+      hand_over(1);
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
     if (ok && nt[w] > 0) ok = mbar_wait_warp(&sm.o_done[w], (nt[w] - 1) & 1, ctl, DETAIL_WAIT_ACCFULL);
