@@ -27,12 +27,14 @@
 // at 16 rows and 39 at 32, where tiles of 64 rows take 46 for both; 4 requests of 900 keys, 16 rows:
 // 12.3 and 16.7. More than 64 rows are several tiles: O^T of 128 would fill TMEM.
 //
-// Bound: for up to 64 rows a request the bytes, 1152 a key. With 128 rows the products (278528 FLOP a
-// key) would take as long, but the two row tiles pull every latent through L2 to two SMs: 32 requests of
-// 10000 to 40000 keys at 128 heads move 2 x 922 MB in 290 us, 6.3 TB/s, what a plain stream of TMA loads
-// of boxes that lie in L2 reaches (6.4). 4 requests of up to 900 keys at 16 heads: 12.9 us, which is two
-// launches and the latency of one tile's chain, TMA to result. Measured against it on the long case: two
-// softmax groups 300 us, the queries in TMEM 298, the tiles fetched into L2 ahead of time 304.
+// Bound: for up to 64 rows a request the bytes, 1152 a key (24 requests of 8000 to 16000 keys, 8 heads:
+// 67 us, 5.0 TB/s). With more, the products of each row tile: a QK of 64 rows and 32 keys reads 3 KB of
+// operands from shared memory in 25 cycles, three times what its FLOPs need, so a tile's 36 take 900
+// cycles and its PV 260 more, of the 1550 that a tile takes: 32 requests of 10000 to 40000 keys at 128
+// heads, 290 us. 4 requests of up to 900 keys at 16 heads: 12 us, which is two launches and the latency of
+// one tile's chain, TMA to result. Measured against it on the long case: two softmax groups 300 us, the
+// queries in TMEM 298, the tiles fetched into L2 ahead of time 304. Tiles of 64 keys would halve the
+// queries' share of the operands, at two tiles in the ring.
 #include <algorithm>
 #include <cmath>
 
