@@ -33,8 +33,8 @@
 // cycles and its PV 260 more, of the 1550 that a tile takes: 32 requests of 10000 to 40000 keys at 128
 // heads, 290 us. 4 requests of up to 900 keys at 16 heads: 12 us, which is two launches and the latency of
 // one tile's chain, TMA to result. Measured against it on the long case: two softmax groups 300 us, the
-// queries in TMEM 298, the tiles fetched into L2 ahead of time 304. Tiles of 64 keys would halve the
-// queries' share of the operands, at two tiles in the ring.
+// queries in TMEM 298, the tiles fetched into L2 ahead of time 304, QKs of two key tiles at once, which
+// read the queries half as often, 331 (a ring of four tiles then leaves nothing to look ahead to).
 #include <algorithm>
 #include <cmath>
 

@@ -28,8 +28,8 @@
 // it: two threads a row (614 us: the pair's exchange and the shared unit take what the shorter rows give),
 // a quarter of the exponentials on the FMA pipe (596), P handed over in parts of 96 and 32 keys (588),
 // exponentials that start with the maximum so far while the tile's is found (635: more registers than
-// there are), tiles fetched into L2 ahead of time (598), K and V blocks of 64 keys in one ring of eight (579, but 142
-// against 137 us for 2048 tokens behind 6144), a rolled softmax that reads S twice (600).
+// there are), tiles fetched into L2 ahead of time (598), V in blocks of 64 keys and K in one ring of eight
+// (579, but 142 against 137 us for 2048 tokens behind 6144), a rolled softmax that reads S twice (600).
 //
 // A call with few query blocks (256 queries of one head) would leave SMs idle, so its blocks' key tiles
 // are split into parts of `chunk` tiles, which write unnormalised O, m and l, and
