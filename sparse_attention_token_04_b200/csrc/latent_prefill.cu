@@ -456,10 +456,12 @@ __global__ void __launch_bounds__(256) latent_prefill_combine_kernel(const LpPar
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, h = blockIdx.x, b = blockIdx.z;
   const int qb = blockIdx.y / (kRows / 32), row = blockIdx.y % (kRows / 32) * 32 + lane;
   const LpBlock u = lp_block(p, b, qb);
+  // Every CTA waits before it exits, also where there is nothing to join: what comes behind this grid on the
+  // stream waits for this grid only, and the grid in front has results of its own to write.
+  grid_dependency_wait();
   if (u.bad || u.i0 + row - lane >= u.nq) return;
   const int parts = lp_parts(p, max(u.tiles(0, p.causal), u.tiles(1, p.causal)));
   if (parts == 1) return;                     // (its CTA has written the results)
-  grid_dependency_wait();
   if (u.i0 + row >= u.nq) return;
   const int64_t unit = ((static_cast<int64_t>(b) * p.n_blocks + qb) * p.H + h) * p.splits * kRows;
   const float2* ml = p.ml + unit + row;
