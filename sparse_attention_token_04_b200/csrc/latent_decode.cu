@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             sm.fac[done % kLdLead][row] = f;
           }
           if (lane == 0) sm.grow[done % kLdLead][warp] = any;
+          tc_fence_before();                    // (the QK issuer takes this as leave to overwrite S)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.m_ready[done % kLdLead]);
           // The next tile's scores, where they are there already; they arrive behind the exponentials.
