@@ -267,7 +267,9 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, c
     if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
   bool ok = true;
   if (lane_id() == 0) ok = mbar_wait_long(smem_u32(bar), parity, ctl.hdr, ctl.abort, ctl.budget_ns, detail);
-  return __shfl_sync(0xFFFFFFFFu, ok, 0);
+  ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+  __syncwarp();  // orders what the other lanes read behind lane 0's wait (a shuffle orders no memory)
+  return ok;
 }
 
 // ------------------------------------------------------------------------------------------

@@ -401,12 +401,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.m_ready[done % kLdLead]);
           // The next tile's scores, where they are there already; they arrive behind the exponentials.
-          have = done + 1 < total;
-          if (have) {
-            bool there = false;
-            if (lane == 0) there = mbar_test(&sm.s_full[s_buf], s_ph);
-            have = __shfl_sync(0xFFFFFFFFu, there, 0);
-          }
+          have = done + 1 < total && __all_sync(0xFFFFFFFFu, mbar_test(&sm.s_full[s_buf], s_ph));
           if (have) {
             tc_fence_after();
             tmem_ld_32x32b_x32(tmem + s_buf * kLdKeys + lanes, s_next);

@@ -50,3 +50,35 @@ def test_consumer_behind_a_planned_split_that_joins_nothing():
     # rounding of the other order of sums
     part, _ = B.dsa_latent_attention_prefill(queries[0], kv[:nk, :, :NOPE], pe[:nk], kv[:nk, :, NOPE:], *args[3:])
     assert (part.float() - want[0][0].float()).abs().max() <= 4 * 2.0 ** -8 * float(kv.float().abs().max())
+
+
+@pytest.mark.parametrize("Hq,q_len,dtype", [(128, 1, torch.bfloat16), (16, 2, torch.float16), (20, 1, torch.bfloat16)])
+def test_decode_under_load_repeats_bit_for_bit(Hq, q_len, dtype):
+    """Calls beside copies that keep the memory busy, so that some of the kernel's waits are short and others
+    long: many requests of many lengths, the same bits every time."""
+    g = torch.Generator().manual_seed(Hq)
+    lens = [int(x) for x in torch.randint(1, 2500, (40,), generator=g)]
+    blocks = [(n + 63) // 64 for n in lens]
+    table = torch.zeros(len(lens), max(blocks), dtype=torch.int32)
+    perm = torch.randperm(sum(blocks), generator=g).to(torch.int32)
+    at = 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    latent = torch.randn(sum(blocks) * 64, 576, generator=g).to(dtype).cuda()
+    q = torch.randn(len(lens), q_len, Hq, 576, generator=g).to(dtype).cuda()
+    args = (q, latent, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 0.08)
+    ws = torch.zeros(B.dsa_latent_attention_decode_workspace_bytes(len(lens), q_len, Hq), dtype=torch.uint8, device="cuda")
+    want, want_lse = B.dsa_latent_attention_decode(*args, workspace=ws)
+    src = torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    dst = torch.empty_like(src)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            dst.copy_(src)
+    outs = [B.dsa_latent_attention_decode(*args, workspace=ws) for _ in range(30)]
+    torch.cuda.synchronize()
+    for out, lse in outs:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert B.dsa_read_device_status(ws) == (0, 0)
