@@ -391,7 +391,8 @@ DSA_API dsa_status dsa_index_cache_read(const uint8_t* k_cache, const float* k_s
  *   q        [B][q_len][Hq][576], element strides q_stride_t (from one token to the next, request
  *            after request), q_stride_h and 1, multiples of 8; 16-byte aligned
  *   latent   [n_blocks * block_size][576], 16-byte aligned; rows at and behind a request's length
- *            are not used, whatever they hold
+ *            are not used, whatever they hold, and a new token's latent that is not finite harms only
+ *            the tokens that see it. Of the rows in front of the new tokens all tokens see each.
  *   block_table [B][max_blocks] i32 (entries past a request's last block are not read)
  *   out      [B][q_len][Hq][512] of q's type;  lse [B][q_len][Hq] f32 or NULL
  * dtype (of q, latent and out) is bf16 or f16. 1 <= q_len <= 8, 1 <= Hq <= 128, block_size a

@@ -127,6 +127,15 @@ __device__ __forceinline__ uint16_t ld_round(float x) {
   return static_cast<uint16_t>(ld_pack<DT>(x, 0.0f));
 }
 
+// Two values with zeros for those that are not finite.
+template <int DT>
+__device__ __forceinline__ uint32_t ld_finite(uint32_t two) {
+  constexpr uint32_t kExp = DT == DSA_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
+  if ((two & kExp) == kExp) two &= 0xFFFF0000u;
+  if ((two >> 16 & kExp) == kExp) two &= 0x0000FFFFu;
+  return two;
+}
+
 // In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
 // are 2^-32 of the largest (and the largest, 2^(8 + kLdLazy), stays far inside its range).
 template <int DT>
@@ -522,16 +531,28 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           }
           tmem_wait_st();
         }
-        if ((t + 1) * kLdKeys > n) {
-          // Rows behind the request's last key hold anything: zero weights must meet zeros.
-          const int key = ctid >> 2;
-          if (key >= n - t * kLdKeys)
+        if ((t + 1) * kLdKeys > n - p.q_len + 1) {
+          // Zero weights must meet finite values: rows behind the request's last key hold anything, and
+          // those of the new tokens are hidden from the tokens in front of them. (A token that sees a
+          // latent which is not finite has it in its score.)
+          ok = mbar_wait_warp(&sm.full[done % kStages], (done / kStages) & 1, ctl, DETAIL_WAIT_KFULL);
+          if (!ok) break;
+          const int key = ctid >> 2, pos = t * kLdKeys + key;
+          if (pos > n - p.q_len) {
 #pragma unroll 1
             for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(sm.ring[done % kStages] + (2 * (ctid & 3) + c) * kLdSlotBytes + key * 128 +
-                                          u * 16) = make_uint4(0, 0, 0, 0);
+              for (int u = 0; u < 8; ++u) {
+                uint4* v = reinterpret_cast<uint4*>(sm.ring[done % kStages] + (2 * (ctid & 3) + c) * kLdSlotBytes +
+                                                    key * 128 + u * 16);
+                if (pos >= n) {
+                  *v = make_uint4(0, 0, 0, 0);
+                } else {
+                  const uint4 x = *v;
+                  *v = make_uint4(ld_finite<DT>(x.x), ld_finite<DT>(x.y), ld_finite<DT>(x.z), ld_finite<DT>(x.w));
+                }
+              }
+          }
           fence_proxy_async_smem();
         }
         tc_fence_before();

@@ -82,3 +82,35 @@ def test_decode_under_load_repeats_bit_for_bit(Hq, q_len, dtype):
     for out, lse in outs:
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert B.dsa_read_device_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("lens,q_len,Hq,block_size", [([70, 130], 3, 8, 64), ([33, 5, 100], 8, 5, 64), ([4000, 9], 4, 16, 64),
+                                                      ([64, 2, 40], 3, 40, 8), ([2000], 2, 128, 64)])
+def test_decode_latents_of_new_tokens_that_are_not_finite(dtype, lens, q_len, Hq, block_size):
+    """A new token whose latent is not finite harms the tokens that see it; the ones in front of it, and the
+    other requests, get the bits that they get with a finite one in its place (their weight on it is 0)."""
+    g = torch.Generator().manual_seed(sum(lens))
+    blocks = [(n + block_size - 1) // block_size for n in lens]
+    table = torch.zeros(len(lens), max(blocks), dtype=torch.int32)
+    for b, n in enumerate(blocks):
+        table[b, :n] = torch.arange(sum(blocks[:b]), sum(blocks[:b]) + n)
+    latent = torch.randn(sum(blocks) * block_size, 576, generator=g).to(dtype)
+    q = torch.randn(len(lens), q_len, Hq, 576, generator=g).to(dtype).cuda()
+    rest = (table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), 0.08)
+    clean, clean_lse = B.dsa_latent_attention_decode(q, latent.cuda(), *rest, block_size=block_size)
+    row = lambda pos: int(table[0, pos // block_size]) * block_size + pos % block_size
+    for first in range(1, q_len):                   # the first of request 0's new tokens that is not finite
+        bad = latent.clone()
+        for i in range(first, q_len):
+            bad[row(lens[0] - q_len + i), [0, 77, 300, 511, 575]] = torch.tensor(
+                [float("nan"), float("inf"), -float("inf"), float("nan"), float("inf")], dtype=dtype)
+        out, lse = B.dsa_latent_attention_decode(q, bad.cuda(), *rest, block_size=block_size)
+        assert torch.equal(out[0, :first], clean[0, :first]) and torch.equal(lse[0, :first], clean_lse[0, :first])
+        assert out[0, first:].isnan().all() and lse[0, first:].isnan().all()
+        assert torch.equal(out[1:], clean[1:]) and torch.equal(lse[1:], clean_lse[1:])
+    # one that is not finite among the values only: NaN scores for those who see it all the same
+    bad = latent.clone()
+    bad[row(lens[0] - 1), 200] = float("nan")
+    out, _ = B.dsa_latent_attention_decode(q, bad.cuda(), *rest, block_size=block_size)
+    assert torch.equal(out[0, :-1], clean[0, :-1]) and out[0, -1].isnan().all()
