@@ -426,7 +426,8 @@ DSA_API dsa_status dsa_latent_attention_decode(const void* q, int64_t q_stride_t
  *   out [Tq][H][128] of q's type;  lse [Tq][H] f32 or NULL
  * d_nope = 128, d_pe = 64 and dv = 128 (else DSA_ERR_UNSUPPORTED); scale > 0. Arithmetic as in the
  * absorbed form. A request's values must be finite where any of its queries sees them. A request
- * with bad offsets or more than max_q queries is recorded as DSA_ERR_DEVICE and left out.
+ * with bad offsets or more than max_q queries is recorded as DSA_ERR_DEVICE and left out. (With
+ * Tq = 0 or max_q = 0 nothing is launched, and no request is looked at.)
  * workspace: >= DSA_WS_HEADER_BYTES bytes, 256-byte aligned. With at least
  * dsa_latent_attention_prefill_workspace_bytes(B, Tq, Tk, max_q, H, causal) bytes the keys of a call with few
  * queries and heads are split over more SMs (its sums are then taken in another order).

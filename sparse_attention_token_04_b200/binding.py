@@ -5,6 +5,12 @@ tensors; the binding checks dtype, device and contiguity, allocates outputs and 
 with torch when the caller does not pass them, and forwards raw pointers and the current
 CUDA stream. All computation happens in the library's kernels; if the library is missing
 this module raises instead of falling back to anything else.
+
+What the kernels find wrong in device-side inputs (a page, a slot, a length, a value that is not
+finite) is recorded in the call's workspace and read with dsa_read_device_status. A call without
+a workspace makes one of its own, and its record is lost with it: dsa_latent_attention_prefill
+then leaves the rows of a request with bad offsets, or with more than max_q queries, unwritten
+without a word.
 """
 
 from __future__ import annotations
