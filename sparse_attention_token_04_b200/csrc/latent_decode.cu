@@ -53,7 +53,10 @@ constexpr int kLdScores = 3;                    // S buffers: two QK products ah
 constexpr int kLdSlotBytes = kLdKeys * 128;     // 4 KB: one chunk
 constexpr int kLdTileBytes = kLdChunks * kLdSlotBytes;
 constexpr int kLdThreads = 352;
-constexpr int kLdLead = 4;                      // rescale factors of this many tiles are kept
+// Tiles whose barriers and rescale factors are kept apart. One of warps 4-7 may be two tiles ahead of
+// another (the softmax hands over the maxima of tile t + 2 before it waits for the PV of tile t): with
+// p_ready of two tiles its arrival there would count for the slow one's at tile t.
+constexpr int kLdLead = 4;
 // Cost of a segment's start and end, in tiles: CTAs that pass from one request to the next get fewer tiles.
 // (20 requests of 100 to 600 keys, 64 rows: 23.1 us with 4, 27.0 with 0; 300 of 1 to 300, 16 rows: 40.8 and
 // 48.0; 8 of 2000 to 16000, 256 rows: 58.2 and 62.9; 2, 6 and 9 are within 5% of 4.)
@@ -69,7 +72,7 @@ struct LdSmem {
   float fac[kLdLead][HT], inv[HT];
   int grow[kLdLead][4];                         // whether a softmax warp's factors are to be applied
   uint64_t full[kStages], empty[kStages];       // empty: the tile's PV is done
-  uint64_t q_full, s_full[kLdScores], m_ready[kLdLead], p_ready[2], seg_ready, seg_done, drain[2];
+  uint64_t q_full, s_full[kLdScores], m_ready[kLdLead], p_ready[kLdLead], seg_ready, seg_done, drain[2];
   uint32_t tmem;
   int abort;
   int b0, tile0, ntiles;                        // this CTA's range
@@ -160,8 +163,10 @@ __global__ void __launch_bounds__(kLdThreads, 1)
     }
     mbar_init(&sm.q_full, 4);
     for (int i = 0; i < kLdScores; ++i) mbar_init(&sm.s_full[i], 1);
-    for (int i = 0; i < kLdLead; ++i) mbar_init(&sm.m_ready[i], kSoft);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_ready[i], kSoft + 4);
+    for (int i = 0; i < kLdLead; ++i) {
+      mbar_init(&sm.m_ready[i], kSoft);
+      mbar_init(&sm.p_ready[i], kSoft + 4);
+    }
     mbar_init(&sm.seg_ready, kSoft);
     mbar_init(&sm.seg_done, 4);
     mbar_init(&sm.drain[0], 1);
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           acc = 0;
         }
         // (A tile whose P is there has landed: its scores came from it.)
-        if (!mbar_wait_call(&sm.p_ready[t & 1], (t >> 1) & 1, ctl, DETAIL_WAIT_SCORES)) break;
+        if (!mbar_wait_call(&sm.p_ready[t % kLdLead], (t / kLdLead) & 1, ctl, DETAIL_WAIT_SCORES)) break;
         tc_fence_after();
         const uint64_t dv = dv0 + st * (kLdTileBytes >> 4), dp = dp0 + (t & 1) * (kLdKeys * 2 >> 4);
 #pragma unroll
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
+          if (lane == 0) mbar_arrive(&sm.p_ready[done % kLdLead]);
           if (have) {
             tmem_wait_ld_regs(s_next);
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready[done & 1]);
+        if (lane == 0) mbar_arrive(&sm.p_ready[done % kLdLead]);
       }
       if (!ok) break;
       // Every QK of the segment is done, so the next one's queries may come.

@@ -3,6 +3,7 @@ consumer right behind it, under load (GPU). Tolerances are those of test_gpu_lat
 there; results of the same arithmetic are compared bit for bit."""
 
 import math
+import random
 
 import pytest
 import torch
@@ -114,3 +115,23 @@ def test_decode_latents_of_new_tokens_that_are_not_finite(dtype, lens, q_len, Hq
     bad[row(lens[0] - 1), 200] = float("nan")
     out, _ = B.dsa_latent_attention_decode(q, bad.cuda(), *rest, block_size=block_size)
     assert torch.equal(out[0, :-1], clean[0, :-1]) and out[0, -1].isnan().all()
+
+
+def test_decode_random_calls():
+    """Calls of random shapes one after another: few and many requests of very uneven lengths, drafted tokens
+    over tile borders, pages of all sizes, so that the kernel's warps meet in ever new orders."""
+    from test_gpu_latent_attention import _check_decode, _decode_case
+
+    rng = random.Random(7)
+    for n in range(120):
+        size = lambda: max(0, int(round(math.exp(rng.uniform(0, math.log(700))))) - rng.choice([0, 0, 1]))
+        lens = [size() for _ in range(rng.choice([1, 2, 3, 7, 33]))]
+        q_len, Hq, block = rng.randint(1, 8), rng.choice([1, 3, 8, 16, 17, 32, 40, 64, 100, 128]), rng.choice([8, 16, 24, 40, 64, 128])
+        q, latent, table, seq, scale = _decode_case(lens, q_len, Hq, block, rng.choice([torch.bfloat16, torch.float16]), n)
+        ws = torch.zeros(B.dsa_latent_attention_decode_workspace_bytes(len(lens), q_len, Hq), dtype=torch.uint8, device="cuda")
+        out, lse = B.dsa_latent_attention_decode(q.cuda(), latent.cuda(), table.cuda(), seq.cuda(), scale,
+                                                 block_size=block, workspace=ws)
+        assert B.dsa_read_device_status(ws) == (0, 0), (lens, q_len, Hq, block)
+        heads, some = sorted({0, Hq // 2, Hq - 1}), sorted(rng.sample(range(len(lens)), min(3, len(lens))))
+        _check_decode(q[some][:, :, heads], latent, table[some], seq[some], scale, block, out[some][:, :, heads],
+                      lse[some][:, :, heads])
