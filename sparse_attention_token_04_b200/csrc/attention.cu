@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_split_kernel(const _
       const uint64_t db = make_smem_desc(smem_u32(sm.stage[st] + kAttHeads * 128), 128);
 #pragma unroll
       for (int kk = 0; kk < kAttChunk / 16; ++kk)
-        tc_mma_bf16(tS, da + 2ull * kk, db + 2ull * kk, make_idesc_bf16(kAttHeads, kAttSplit),
+        tc_mma_16(tS, da + 2ull * kk, db + 2ull * kk, make_idesc_bf16(kAttHeads, kAttSplit),
                     (ch > 0 || kk > 0) ? 1u : 0u);
       tc_commit(&sm.qk_done[st]);
     }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_split_kernel(const _
         for (int kk = 0; kk < kAttPvKeys / 16; ++kk) {
           const uint64_t db = make_smem_desc_mn(vbase + half * 4 * kAttPvBlockBytes + kk * 2048,
                                                 kAttPvBlockBytes, 1024);
-          tc_mma_bf16(half == 0 ? tO : tS, da + 2ull * ((i & 1) * 2 + kk), db, idesc_pv,
+          tc_mma_16(half == 0 ? tO : tS, da + 2ull * ((i & 1) * 2 + kk), db, idesc_pv,
                       (i > 0 || kk > 0) ? 1u : 0u);
         }
       }

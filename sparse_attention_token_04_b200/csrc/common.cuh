@@ -7,6 +7,8 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/dsa_indexer.h"
@@ -463,8 +465,9 @@ __device__ __forceinline__ uint64_t make_smem_desc_mn(uint32_t smem_addr, uint32
   return desc;
 }
 
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem], 16-bit inputs of the one type that the descriptor names.
+__device__ __forceinline__ void tc_mma_16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
@@ -494,8 +497,7 @@ __host__ __device__ constexpr uint32_t make_idesc_16(uint32_t bf16, uint32_t M, 
   return (1u << 4) | (bf16 << 7) | (bf16 << 10) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
-// As tc_mma_bf16 (the descriptor says which of the 16-bit types), with the A operand in TMEM: lane
-// m, 32-bit column c holds A[m][2c], A[m][2c + 1].
+// As tc_mma_16, with the A operand in TMEM: lane m, 32-bit column c holds A[m][2c], A[m][2c + 1].
 __device__ __forceinline__ void tc_mma_16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
@@ -561,6 +563,23 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "l"(reinterpret_cast<const uint64_t&>(a)), "l"(reinterpret_cast<const uint64_t&>(b)), "l"(reinterpret_cast<const uint64_t&>(c)));
   return reinterpret_cast<const float2&>(r);
 }
+
+// Two values of a 16-bit type, rounded to nearest.
+template <int DT>
+__device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
+  if constexpr (DT == DSA_DTYPE_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// In f16 a softmax numerator is scaled by 2^8, so that the ones that vanish below the type's smallest
+// value are 2^-32 of the largest. (A running maximum may lag by 2^6: 2^14 stays far inside its range.)
+template <int DT>
+constexpr float kNumeratorShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
 
 // 2^x (2 ulp; denormal results as 0).
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -38,9 +38,6 @@
 #include <algorithm>
 #include <cmath>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -116,18 +113,8 @@ __device__ __forceinline__ int64_t ld_work_before(const LdParams& p, int n, int 
 __device__ __forceinline__ int64_t ld_sharers(int64_t T, int n_cta) { return T < n_cta ? (T > 0 ? T : 1) : n_cta; }
 
 template <int DT>
-__device__ __forceinline__ uint32_t ld_pack(float lo, float hi) {
-  if constexpr (DT == DSA_DTYPE_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-template <int DT>
 __device__ __forceinline__ uint16_t ld_round(float x) {
-  return static_cast<uint16_t>(ld_pack<DT>(x, 0.0f));
+  return static_cast<uint16_t>(pack_16<DT>(x, 0.0f));
 }
 
 // Two values with zeros for those that are not finite.
@@ -138,11 +125,6 @@ __device__ __forceinline__ uint32_t ld_finite(uint32_t two) {
   if ((two >> 16 & kExp) == kExp) two &= 0x0000FFFFu;
   return two;
 }
-
-// In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
-// are 2^-32 of the largest (and the largest, 2^(8 + kLdLazy), stays far inside its range).
-template <int DT>
-constexpr float kLdShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
 
 template <int DT, int HT>
 __global__ void __launch_bounds__(kLdThreads, 1)
@@ -312,7 +294,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         for (int c = 0; c < kLdChunks; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(tmem + buf * kLdKeys, dq + (c * HT * 128 >> 4) + 2ull * kk,
+            tc_mma_16(tmem + buf * kLdKeys, dq + (c * HT * 128 >> 4) + 2ull * kk,
                         dk + (c * kLdSlotBytes >> 4) + 2ull * kk, idesc, c > 0 || kk > 0 ? 1u : 0u);
         tc_commit(&sm.s_full[buf]);
         --left;
@@ -346,7 +328,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int kk = 0; kk < kLdKeys / 16; ++kk)
-            tc_mma_bf16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc,
+            tc_mma_16(tO + mt * HT, dv + (mt * 2 * kLdSlotBytes + kk * 2048 >> 4), dp + 2ull * kk, idesc,
                         kk > 0 ? 1u : acc);
         tc_commit(&sm.empty[st]);
         --left;
@@ -422,7 +404,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
           }
           if (done >= 2) ok = pv_done(done - 2);  // P's half of the buffer is free
           if (mine) {
-            const float base = m == -INFINITY ? 0.0f : kLdShift<DT> - m * p.scale_log2;
+            const float base = m == -INFINITY ? 0.0f : kNumeratorShift<DT> - m * p.scale_log2;
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -433,7 +415,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
                 const float p1 = exp2_fast(fmaf(__uint_as_float(s[u * 8 + e + 1]), p.scale_log2, base));
                 sum[e & 2] += p0;
                 sum[(e & 2) + 1] += p1;
-                w4[e >> 1] = ld_pack<DT>(p0, p1);
+                w4[e >> 1] = pack_16<DT>(p0, p1);
               }
               *reinterpret_cast<uint4*>(sm.p + sw128(row, (done & 1) * 4 + u)) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
             }
@@ -458,7 +440,7 @@ __global__ void __launch_bounds__(kLdThreads, 1)
             sm.inv[row] = l != 0.0f ? 1.0f / l : 0.0f;
             if (p.lse && r < R)
               p.lse[static_cast<int64_t>(b) * R + r] =
-                  l != 0.0f ? m * p.scale + (logf(l) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+                  l != 0.0f ? m * p.scale + (logf(l) - kNumeratorShift<DT> * 0.69314718055994531f) : -INFINITY;
           } else {
             float* ml = p.ml + ((static_cast<int64_t>(ht) * gridDim.y + cta) * 2 + (t_first == 0)) * 2 * HT;
             ml[row] = m;
@@ -690,7 +672,7 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
       const float inv = L != 0.0f ? 1.0f / L : 0.0f;
       for (int c = c_first; c < ns; c += kPer) wt[c * HT + row] *= inv;
       if (lse && blockIdx.z == 0 && c_first == 0 && row < rows)
-        lse[row] = L != 0.0f ? M * p.scale + (logf(L) - kLdShift<DT> * 0.69314718055994531f) : -INFINITY;
+        lse[row] = L != 0.0f ? M * p.scale + (logf(L) - kNumeratorShift<DT> * 0.69314718055994531f) : -INFINITY;
     }
     __syncthreads();
     {
@@ -718,7 +700,7 @@ __global__ void __launch_bounds__(256) latent_combine_kernel(const LdParams p, i
     __syncthreads();
     for (int i = tid; i < rows * kDims / 2; i += 256) {
       const int h = i / (kDims / 2), d = i % (kDims / 2) * 2;
-      *reinterpret_cast<uint32_t*>(out + h * kLdDv + d) = ld_pack<DT>(tile[h * kPitch + d], tile[h * kPitch + d + 1]);
+      *reinterpret_cast<uint32_t*>(out + h * kLdDv + d) = pack_16<DT>(tile[h * kPitch + d], tile[h * kPitch + d + 1]);
     }
     __syncthreads();
   }

@@ -40,9 +40,6 @@
 #include <algorithm>
 #include <cmath>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "common.cuh"
 #include "internal.h"
 
@@ -103,22 +100,6 @@ __device__ __forceinline__ LpBlock lp_block(const LpParams& p, int b, int qb) {
 }
 // CTAs that share the n key tiles of a block.
 __device__ __forceinline__ int lp_parts(const LpParams& p, int n) { return n <= p.chunk ? 1 : (n + p.chunk - 1) / p.chunk; }
-
-template <int DT>
-__device__ __forceinline__ uint32_t pack_16(float lo, float hi) {
-  if constexpr (DT == DSA_DTYPE_BF16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-// In f16 a numerator is scaled by 2^8, so that the ones that vanish below the type's smallest value
-// are 2^-32 of the largest (and the largest, 2^(8 + kLpLazy), stays far inside its range).
-template <int DT>
-constexpr float kLpShift = DT == DSA_DTYPE_F16 ? 8.0f : 0.0f;
 
 // kSplit: a block's key tiles are shared by up to p.splits CTAs.
 template <int DT, bool kSplit>
@@ -244,7 +225,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
           const uint64_t da = make_smem_desc(smem_u32(sm.q[w][c]), 128), db = dk + slot * (kLpBlock >> 4);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16(tmem + w * 128, da + 2ull * kk, db + 2ull * kk, idesc_qk, (c > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_16(tmem + w * 128, da + 2ull * kk, db + 2ull * kk, idesc_qk, (c > 0 || kk > 0) ? 1u : 0u);
           if (last) tc_commit(&sm.k_free[slot]);
         }
         tc_commit(&sm.s_full[w]);
@@ -292,7 +273,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + w * 128 + lanes, tO = tmem + 256 + w * 128 + lanes;
     const int n_row = u.sees(i, p.causal) - skip, n_warp = u.sees(first, p.causal) - skip;
-    constexpr float kShift = kLpShift<DT>;
+    constexpr float kShift = kNumeratorShift<DT>;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < nt[w]; ++j) {
@@ -503,7 +484,7 @@ __global__ void __launch_bounds__(256) latent_prefill_combine_kernel(const LpPar
   dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
   dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   if (warp == 0 && p.lse)
-    p.lse[at] = L != 0.0f ? M * p.scale + (logf(L) - kLpShift<DT> * 0.69314718055994531f) : -INFINITY;
+    p.lse[at] = L != 0.0f ? M * p.scale + (logf(L) - kNumeratorShift<DT> * 0.69314718055994531f) : -INFINITY;
 }
 
 static int64_t lp_blocks(int max_q, int Tq) { return (static_cast<int64_t>(std::min(max_q, Tq)) + 2 * kLpTile - 1) / (2 * kLpTile); }
