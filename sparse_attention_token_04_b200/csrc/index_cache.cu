@@ -6,9 +6,10 @@
 // with the row's values in fp32 after the rotation (not rounded to the input's type in between),
 // both divisions IEEE fp32 and the code rounded to nearest even. Bound by HBM (long inputs) or by
 // one launch (a decode step): each value is read once and kept in registers between the row's
-// maximum and its codes. 16384 tokens of 64 heads x 128, bf16, half of each head rotated: 87 us,
-// 4.6 TB/s, and the instructions of the rotation, the maximum and the quotient then take two thirds of
-// the issue slots. 32 keys of 128 into the cache: 4.0 us.
+// maximum and its codes. 16384 tokens of 64 heads x 128, bf16, half of each head rotated: 89 us,
+// 4.5 TB/s, where neither is full (62% of the issue slots, DRAM at 52%): with 20 warps an SM a row's loads,
+// its maximum over the CTA and its codes follow one another. 32 keys of 128 into the cache: 2.8 us. The
+// instance for rows of more than four passes is far slower (below).
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
@@ -44,8 +45,8 @@ __device__ __forceinline__ float max_or_nan(float a, float b, float c) {
 // the IBM RISC System/6000 processor", 1990), as long as nothing underflows, which kLeastScale sees to.
 // Checked against divisions next to every border between two codes. (Products that were checked against
 // the borders and divided where close cost more: bf16 values meet borders exactly often enough that
-// every third warp divided. Without the correction the row of 64 heads above took 83 us, with it 94, two
-// values at a time 87; the rotary kernel, bound by HBM, gained nothing from turning two at a time.)
+// every third warp divided. The correction cost the rows of 64 heads above 13%, two values at a time gave
+// half of that back; the rotary kernel, bound by HBM, gained nothing from turning two at a time.)
 constexpr float kLeastScale = 0x1p-90f;
 __device__ __forceinline__ float2 quotient(float2 v, float scale, float inv) {
   const float2 q = mul2(v, make_float2(inv, inv));
@@ -224,9 +225,9 @@ __global__ void __launch_bounds__(kQuantThreads) index_quantise_small_kernel(con
 // the same item of another head: it finds its offsets once. A row's values stay packed as they were
 // loaded; rotated ones are rotated twice, for the maximum and for the codes. (With the next row's
 // loads on their way while this one's are worked on, which leaves registers for four CTAs an SM instead
-// of five, the row of 64 heads below takes 99 to 124 us.) One barrier a row: in front of it a warp leaves its maximum (two
-// buffers) and the first threads the next row's (cos, sin) (three, since the rare paths read them behind
-// it).
+// of five, the row of 64 heads above takes 11 to 40% longer.) One barrier a row: in front of it a warp leaves
+// its maximum (two buffers) and the first threads the next row's (cos, sin) (three, since the rare paths read
+// them behind it).
 template <int DT, bool INTERLEAVED, int NI>
 __global__ void __launch_bounds__(kQuantThreads, NI <= 4 ? 5 : 1)
     index_quantise_kernel(const __grid_constant__ QuantParams p) {
@@ -359,10 +360,12 @@ static int quantise_passes(const QuantParams& p) {
 template <int DT, bool INTERLEAVED>
 static dsa_status launch_quantise_t(const QuantParams& p, int num_sms, cudaStream_t stream) {
   const int n = p.H * (p.d / kItem);
-  // As few threads a row as it has items (16384 keys of 128: 6.8 us with 8 threads, 14.9 with 32), but few
-  // rows are spread over more CTAs (32 keys of 128: 2.5 us with 32, 3.3 with 8). The instance of 18 passes
-  // takes any larger row, with registers for fewer CTAs (1024 tokens of 64 heads x 128: 24 us, 8.0 in the
-  // one of four).
+  // As few threads a row as it has items (16384 keys of 128: 6.8 us with 8 threads, 12.6 with 32), but few
+  // rows are spread over more CTAs (32 keys of 128: 2.6 us with 32, 3.2 with 8). The instance of 18 passes
+  // takes every row of more than four: rows of more than 512 items, and smaller ones whose rotated and
+  // copied items each leave a pass part empty (64 heads x 128 with a rotary part of 16, 32, 48, 80, 96 or
+  // 112: five or more). Its 255 registers leave two CTAs an SM: 16384 tokens of 64 heads x 128 take 310 us
+  // with 32 dims rotated, and 89 in the instance of four with 64.
   if (n <= 32 && p.T <= kQuantFewRows) return launch_quantise_small<DT, INTERLEAVED, 32>(p, stream);
   if (n <= 8) return launch_quantise_small<DT, INTERLEAVED, 8>(p, stream);
   if (n <= 16) return launch_quantise_small<DT, INTERLEAVED, 16>(p, stream);
@@ -385,7 +388,7 @@ dsa_status launch_quantise(const QuantParams& p, int num_sms, int dtype, cudaStr
 // ------------------------------------------------------------------------------------------
 // Cache read. A CTA takes kReadRows output rows: its first threads find each row's request (a
 // binary search over the row offsets) and cache row, then all copy 16 codes at a time. Bound by HBM:
-// 32 requests of 10000 to 200000 keys of 128 dims as bf16 values take 200 us, 5.4 TB/s; three prefixes of
+// 32 requests of 10000 to 200000 keys of 128 dims as bf16 values take 204 us, 5.3 TB/s; three prefixes of
 // up to 1500 keys as codes and scales 3.1 us, one launch.
 // ------------------------------------------------------------------------------------------
 constexpr int kReadThreads = 256;

@@ -21,18 +21,19 @@
 //   warp 8     TMA: a tile as one box of nine 64-dim chunks of 4 KB, into a ring of four or five tiles;
 //   warp 9     one thread issues the QK products, up to three tiles ahead of the softmax;
 //   warp 10    one thread issues the PV products. (With both in one thread the tensor core idled while
-//              that thread looked at its barriers: 361 us instead of 356 on the long case below.)
+//              that thread looked at its barriers: 1.4% more time on the long case below.)
 //
-// Row tiles of 16, 32 or 64 rows: the fewest rows that hold a request's. 16 requests of 8000 keys: 36 us
-// at 16 rows and 39 at 32, where tiles of 64 rows take 46 for both; 4 requests of 900 keys, 16 rows:
-// 12.3 and 16.7. More than 64 rows are several tiles: O^T of 128 would fill TMEM.
+// Row tiles of 16, 32 or 64 rows: the fewest rows that hold a request's. 16 requests of 8000 keys: 36.5 us
+// at 16 rows and 39.6 at 32, where tiles of 64 rows take 48 for both; 4 requests of 900 keys, 16 rows:
+// 13.4, and 18.8 in tiles of 64. More than 64 rows are several tiles: O^T of 128 would fill TMEM.
 //
 // Bound: for up to 64 rows a request the bytes, 1152 a key (24 requests of 8000 to 16000 keys, 8 heads:
-// 67 us, 5.0 TB/s). With more, the products of each row tile: a QK of 64 rows and 32 keys reads 3 KB of
+// 62 us, 5.0 TB/s). With more, the products of each row tile: a QK of 64 rows and 32 keys reads 3 KB of
 // operands from shared memory in 25 cycles, three times what its FLOPs need, so a tile's 36 take 900
 // cycles and its PV 260 more, of the 1550 that a tile takes: 32 requests of 10000 to 40000 keys at 128
-// heads, 290 us. 4 requests of up to 900 keys at 16 heads: 12 us, which is two launches and the latency of
-// one tile's chain, TMA to result. Measured against it on the long case: two softmax groups 300 us, the
+// heads, 335 us back to back, which the power limit holds at 1700 MHz (300 to 320 from idle). 4 requests of
+// up to 900 keys at 16 heads: 13 us, which is two launches and the latency of one tile's chain, TMA to
+// result. Measured against it on the long case, where it took 292 us from idle: two softmax groups 300, the
 // queries in TMEM 298, the tiles fetched into L2 ahead of time 304, QKs of two key tiles at once, which
 // read the queries half as often, 331 (a ring of four tiles then leaves nothing to look ahead to).
 #include <algorithm>
@@ -55,8 +56,8 @@ constexpr int kLdThreads = 352;
 // p_ready of two tiles its arrival there would count for the slow one's at tile t.
 constexpr int kLdLead = 4;
 // Cost of a segment's start and end, in tiles: CTAs that pass from one request to the next get fewer tiles.
-// (20 requests of 100 to 600 keys, 64 rows: 23.1 us with 4, 27.0 with 0; 300 of 1 to 300, 16 rows: 40.8 and
-// 48.0; 8 of 2000 to 16000, 256 rows: 58.2 and 62.9; 2, 6 and 9 are within 5% of 4.)
+// (20 requests of 100 to 600 keys, 64 rows: 21.2 us with 4, 24.8 with 0; 300 of 1 to 300, 16 rows: 42.8 and
+// 49.7; 12 of 300 to 5000, 128 rows: 35.9 and 36.9; 2, 6 and 9 are within 5% of 4.)
 constexpr int kLdSegment = 4;
 constexpr float kLdLazy = 6.0f;
 

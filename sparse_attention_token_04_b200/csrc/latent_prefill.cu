@@ -16,27 +16,30 @@
 //                   down the one tensor pipe in issue order.
 // Shared memory: 96 KB of Q, 64 KB of K, 64 KB of V, all [128 rows][64 dims] blocks with the 128-byte
 // swizzle. (With K two tiles and V one tile deep instead, a V tile came 1000 cycles late every time; in
-// one ring of blocks for both, V's two blocks are not neighbours and PV takes twice the MMAs: 658 us
-// where this takes 586.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and
+// one ring of blocks for both, V's two blocks are not neighbours and PV takes twice the MMAs: 12% more time
+// on the long prompt below.) TMEM: S (and P) of the two tiles in columns 0-127 and 128-255, O in 256-383 and
 // 384-511. P goes over in two halves of 64 keys, so that PV starts behind the first.
 //
 // Bound: the chain of one query tile. The MMAs of a key tile take 2560 cycles for both query tiles, but
 // S and P share columns, so a tile's next QK waits for its PV: from scores to scores its softmax (2200
 // cycles: 700 to read S and find the maximum, 1500 for the exponentials, whose unit both tiles share),
-// its own products (1280) and some 600 of hand-over follow one another, 4300 cycles in all. 580 us for a
-// prompt of 8192 tokens and 32 heads, bf16: 1190 TFLOP/s, 73% of the cuBLAS burst rate. Measured against
-// it: two threads a row (614 us: the pair's exchange and the shared unit take what the shorter rows give),
-// a quarter of the exponentials on the FMA pipe (596), P handed over in parts of 96 and 32 keys (588),
-// exponentials that start with the maximum so far while the tile's is found (635: more registers than
-// there are), tiles fetched into L2 ahead of time (598), V in blocks of 64 keys and K in one ring of eight
-// (579, but 142 against 137 us for 2048 tokens behind 6144), a rolled softmax that reads S twice (600).
+// its own products (1280) and some 600 of hand-over follow one another, 4300 cycles in all. A prompt of
+// 8192 tokens and 32 heads, bf16: 667 us back to back, which the power limit holds at 1545 MHz: 1030
+// TFLOP/s, 75% of the sustained cuBLAS rate (590 us from idle, 71% of the burst rate). The tensor pipe is
+// then active in 61% of the cycles, the exponentials' unit in 49%. Measured against it, where it took 578 us
+// from idle: two threads a row (614: the pair's exchange and the shared unit take what the shorter rows
+// give), a quarter of the exponentials on the FMA pipe (596), P handed over in parts of 96 and 32 keys
+// (588), exponentials that start with the maximum so far while the tile's is found (635: more registers than
+// there are; the 168 already spill 64 bytes), tiles fetched into L2 ahead of time (598), V in blocks of 64
+// keys and K in one ring of eight (579, but 4% more for 2048 tokens behind 6144), a rolled softmax that
+// reads S twice (600).
 //
 // A call with few query blocks (256 queries of one head) would leave SMs idle, so its blocks' key tiles
 // are split into parts of `chunk` tiles, which write unnormalised O, m and l, and
 // latent_prefill_combine_kernel joins them. lp_plan chooses the chunk. 100 queries behind 8000 keys, 16
-// heads: 129 us whole, 27 split; 2500 tokens of one head: 50 and 17; 2048 tokens behind 6144, 16 heads
-// (128 blocks, 49 to 64 tiles long): 149 and 133. Three requests of 1300 tokens at 8 heads, which the
-// rule leaves whole: 30.3, 36.8 split.
+// heads: 125 us whole, 31 split; 2500 tokens of one head: 48 and 18; 2048 tokens behind 6144, 16 heads
+// (128 blocks, 49 to 64 tiles long): 165 and 162 at the power limit, 169 and 157 from idle. Three requests of
+// 1300 tokens at 8 heads, which the rule leaves whole: 30 us, a fifth more split.
 #include <algorithm>
 #include <cmath>
 
@@ -50,8 +53,8 @@ constexpr int kLpThreads = 320;
 constexpr int kLpBlock = kLpTile * 128;      // 16 KB: 128 rows x 64 dims
 constexpr int kLpKRing = 4;                  // blocks of the K ring (a tile has three)
 constexpr float kLpLazy = 6.0f;              // log2 growth of a row's maximum that is left unscaled
-// Splitting: key tiles of a part at least (2500 tokens of one head: 17.3 us with two, 23.3 with one, 20.6
-// with three), tiles that a split has to save (one, two and three measure alike), parts of a block and
+// Splitting: key tiles of a part at least (2500 tokens of one head: with one 35% more time than with two,
+// with three 19%), tiles that a split has to save (one, two and three measure alike), parts of a block and
 // places for parts per SM (133 KB each) at most.
 constexpr int kLpMinTiles = 2, kLpMinGain = 2, kLpMaxSplits = 32, kLpMaxPlaces = 6;
 

@@ -3,8 +3,9 @@
 // The operator moves its bytes once and computes little, so it is bound by HBM (long inputs) or by
 // one launch (a decode step). A CTA takes one token: its threads start the loads of their first
 // items, then form the token's rot/2 (cos, sin) pairs once in shared memory for all of its heads.
-// 16384 tokens of 64 heads x 128, bf16: 95.6 us, 5.6 TB/s. 32 tokens of 128 heads x 64 in rows of 576:
-// 2.9 us.
+// 16384 tokens of 64 heads x 128, bf16: 97.7 us, 5.5 TB/s. 32 tokens of 128 heads x 64 in rows of 576:
+// 2.8 us. A token of few items leaves most of its CTA idle: 16384 tokens of one head x 64 take 27 us, where
+// their bytes take 0.6.
 #include <cmath>
 
 #include "rotary.cuh"
@@ -48,7 +49,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(RotaryArgs r, const
 }
 
 // Any even rot, any d, strides and alignment: a thread takes one pair or one copied element. (4096
-// tokens of 16 heads x 128, bf16: 17.7 us, the kernel above 10.0.)
+// tokens of 16 heads x 128, bf16: 18.0 us, the kernel above 10.2.)
 template <int DT>
 __global__ void __launch_bounds__(kRotThreads) rotary_any_kernel(RotaryArgs r, const typename Elem<DT>::T* x,
                                                                  int64_t xs_t, int64_t xs_h, typename Elem<DT>::T* out,
@@ -90,7 +91,7 @@ static dsa_status launch_rotary_t(const RotaryLaunch& a) {
   const size_t smem = static_cast<size_t>(a.r.rot / 2) * sizeof(float2);
   const int64_t n = static_cast<int64_t>(a.H) * (wide ? (in_place ? a.r.rot : a.d) / kItem : a.d - a.r.rot / 2);
   // Few tokens: a token's items are spread over CTAs until the GPU has one CTA per SM (32 tokens of 128
-  // heads x 64: 2.5 us, 3.1 with one CTA a token).
+  // heads x 64: 7% more time with one CTA a token).
   const int64_t fill = (a.num_sms + a.T - 1) / a.T, need = (n + kRotThreads - 1) / kRotThreads;
   const dim3 grid(a.T, static_cast<unsigned>(need < fill ? need : fill));
   if (wide && a.r.interleaved)
